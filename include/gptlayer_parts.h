@@ -187,6 +187,171 @@ int gptl_colsum(int rows, int n, int groups, long long ld, long long gstride, gp
 int gptl_colsum_noalloc(int rows, int n, int groups, long long ld, long long gstride,
                         gptl_dtype dtype, const void *a, float *out, gptl_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Norm and rotation of queries and keys, between the QKV product and
+ * attention.  (The Megatron-LM pages give the layer no positions; these
+ * calls, dropout and the token log probabilities below have no counterpart
+ * there.)
+ *
+ * A packed row holds q_heads query heads, then k_heads key heads, then
+ * v_heads value heads, head_dim elements each: the [Q_i | K_i | V_i] rows that
+ * gptl_attention_fwd reads, with groups = tp.  For every query and key head x
+ * of every token:
+ *   n = x * g / sqrt(mean(x^2) + eps)       g = gq for queries, gk for keys
+ *                                           (n = x when both are NULL)
+ *   for each pair j < rot_dim/2 of elements (a, b) of n's first rot_dim:
+ *     phi = 2 pi * pos[axis_j][token] * turns_j
+ *     y_a = n_a cos(phi) - n_b sin(phi),   y_b = n_b cos(phi) + n_a sin(phi)
+ *   the other elements of y are those of n.
+ * Statistics and rotation are fp32, the angle's turns are reduced in fp64
+ * (exact to fp32 for every int position), and y is rounded once.
+ * interleaved = 0 pairs elements (j, j + rot_dim/2), 1 pairs (2j, 2j + 1). */
+typedef struct {
+  int tokens, groups;              /* rows of each group, groups (tp shards)  */
+  int q_heads, k_heads, v_heads;   /* of one group; v_heads may be 0          */
+  int head_dim;                    /* multiple of 16, at most 256             */
+  int rot_dim;                     /* multiple of 16, 0 .. head_dim           */
+  int interleaved;                 /* 0 or 1                                  */
+  int axes;                        /* position axes, 1 .. 4                   */
+  int seq;                         /* pos NULL: every axis is token % seq     */
+  float eps;                       /* > 0 when there are gains                */
+  /* element (group, token, c) of x is at x + group*x_gstride + token*x_ld + c,
+   * of y at y + group*y_gstride + token*y_ld + c: multiples of 8, 0 for dense
+   * (ld = row width, gstride = tokens*ld) */
+  long long x_ld, x_gstride, y_ld, y_gstride;
+} gptl_qk_desc;
+
+/* One rotated pair: its turns (radians / 2 pi) for one step of its axis, and
+ * the axis.  A program lays a table of rot_dim/2 of them out once, in DEVICE
+ * memory, 16-byte aligned. */
+typedef struct {
+  double turns;
+  int axis;
+  int reserved;                    /* 0 */
+} gptl_rope_pair;
+
+/* Fills the host array table[rot_dim/2] for rotary positions with `base`:
+ * axis a takes the next axis_pairs[a] pairs (their sum is rot_dim/2; NULL with
+ * axes = 1).  per_axis = 0: turns_j = base^(-2j/rot_dim) / 2 pi over the whole
+ * table, as for text with (time, height, width) positions; 1: each axis has a
+ * ladder of its own, base^(-i/axis_pairs[a]) / 2 pi for its i-th pair, as for
+ * the rows and columns of an image.  No device work.  GPTL_E_SHAPE for sizes
+ * that do not fit, GPTL_E_ARG unless base > 0 is finite. */
+int gptl_rope_table(int rot_dim, int axes, const int *axis_pairs, int per_axis, double base,
+                    gptl_rope_pair *table);
+
+/* Forward: x -> y.  y is x itself (same strides: in place; V columns are left
+ * alone) or does not overlap it (V columns are copied, so that y is the whole
+ * buffer that attention reads; training keeps x for the backward).  Columns
+ * between the row width and ld are not touched.
+ * gq, gk: [head_dim] (cdt), both or neither.  pos: int32 [axes][tokens] or
+ * NULL.  table: [rot_dim/2], may be NULL when rot_dim is 0; an axis outside
+ * [0, axes) sets bit 2 of the device error word and counts as axis 0.
+ * GPTL_E_SHAPE for sizes or strides outside the limits above, rows that
+ * overlap or seq < 1 without pos; GPTL_E_ARG for eps, interleaved or an overlap
+ * of x and y. */
+int gptl_qk_norm_rope_fwd(const gptl_qk_desc *d, gptl_dtype dtype, const void *x, void *y,
+                          const void *gq, const void *gk, const int *pos,
+                          const gptl_rope_pair *table, gptl_stream_t stream);
+
+/* Scratch bytes gptl_qk_norm_rope_bwd needs when there are gains (0 for a
+ * descriptor outside the limits). */
+size_t gptl_qk_norm_rope_scratch_bytes(const gptl_qk_desc *d);
+
+/* Backward: dx from the forward's x (x strides) and dy, the gradient of y.  dy
+ * and dx have the y strides; dx is dy itself (V columns are left alone) or
+ * overlaps neither dy nor x (V columns are copied).  dgq, dgk: fp32
+ * [head_dim], overwritten with the sums over all tokens, groups and heads, in
+ * a fixed order; given exactly when gq and gk are, as is scratch. */
+int gptl_qk_norm_rope_bwd(const gptl_qk_desc *d, gptl_dtype dtype, const void *x, const void *dy,
+                          void *dx, const void *gq, const void *gk, const int *pos,
+                          const gptl_rope_pair *table, float *dgq, float *dgk, void *scratch,
+                          gptl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Dropout from a counter-based generator: the mask is a function of the state
+ * below, the call's site and the element's place, so it is never stored and
+ * the backward makes it again.
+ *
+ * Element e of the 8-element block v (v = (row*h + column) / 8) of a call is
+ * dropped when the 16-bit number u_e < D, D = floor(p * 65536 + 1/2), where
+ * u_e is half e % 2 (low first) of word e / 2 of Philox4x32-10 (Salmon et al.,
+ * SC 2011) with key = seed and counter words (v, site, offset low, offset
+ * high).  A kept element is multiplied by 65536 / (65536 - D), the inverse of
+ * the exact probability of keeping it. */
+typedef struct {
+  unsigned long long seed, offset;
+} gptl_rng_state;                  /* DEVICE memory, caller-initialised       */
+
+/* offset += n on the device (one thread), once per training step: a captured
+ * step then draws new masks at each replay.  Within a step, give every call
+ * (layer and place) a `site` of its own; a backward takes its forward's site
+ * and runs before the state is advanced. */
+int gptl_rng_advance(gptl_rng_state *rng, unsigned long long n, gptl_stream_t stream);
+
+/* y = resid + dropout(x + bias) over [rows][h]: x (cdt) is the output of a
+ * row-split product without its bias; bias [h] (cdt) and resid (fp32 when
+ * resid_f32, else cdt) may be NULL; y is fp32 when y_f32, else cdt.  The sum is
+ * fp32, rounded once.  y may be x or resid itself where their types agree, and
+ * overlaps no input otherwise.  h % 8 == 0, rows*h < 2^35 (GPTL_E_SHAPE);
+ * 0 <= p and floor(p * 65536 + 1/2) < 65536 (GPTL_E_ARG); p = 0 reads no
+ * state.  rng may be NULL only for p = 0. */
+int gptl_dropout_add_fwd(int rows, int h, gptl_dtype dtype, const void *x, const void *bias,
+                         const void *resid, int resid_f32, float p, const gptl_rng_state *rng,
+                         unsigned site, void *y, int y_f32, gptl_stream_t stream);
+
+/* Scratch bytes gptl_dropout_add_bwd needs for dbias (0 for bad sizes). */
+size_t gptl_dropout_scratch_bytes(int rows, int h);
+
+/* dx (cdt) = dy where kept, times the forward's factor, else 0; dbias (fp32
+ * [h], may be NULL, else scratch is needed) = the column sums of that product
+ * before it is rounded to dx, in a fixed order.  dy is fp32 when dy_f32, else
+ * cdt; dx may be dy itself where the types agree.  The gradient of resid is dy.
+ * Other arguments and errors as the forward's. */
+int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int dy_f32, float p,
+                         const gptl_rng_state *rng, unsigned site, void *dx, float *dbias,
+                         void *scratch, gptl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens under softmax(logits), with the entropy
+ * and the top alternatives, in one pass over the logits.
+ *   logits: [rows] of vocab elements, ld elements apart (ld >= vocab, any
+ *           value), fp32 when logits_f32, else cdt
+ *   m = max_v x_v,  Z = sum_v exp(x_v - m)
+ *   logp    = x_target - m - ln Z
+ *   entropy = ln Z - sum_v p_v (x_v - m),   p_v = exp(x_v - m) / Z
+ *   stats   = (m, ln Z), what the backward needs
+ *   top     : the top_k largest x_v in falling order, equal ones by rising
+ *             index: top_logp = x_v - m - ln Z and top_id = v, [rows][top_k]
+ * All outputs are fp32 (top_id int32).  target: int32 [rows]; a negative one
+ * means none (logp = 0); one >= vocab sets bit 2 of the device error word and
+ * gives logp = NaN.  target and logp come together or not at all; entropy,
+ * stats and the top pair (with top_k = 0) are optional, but one output is
+ * given.  0 <= top_k <= 32 and <= vocab (GPTL_E_ARG); 1 <= vocab < 2^30,
+ * rows >= 1 (GPTL_E_SHAPE).
+ * x_v = -inf has probability 0.  A row of nothing else gives m = ln Z = -inf,
+ * entropy 0, logp and top_logp -inf, top_id 0, 1, ...  A row with +inf or NaN
+ * gives NaN in every output (m: +inf or NaN's row maximum) and top_id -1. */
+int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, int logits_f32,
+                           const void *logits, const int *target, float *logp, float *entropy,
+                           float *stats, int top_k, float *top_logp, int *top_id,
+                           gptl_stream_t stream);
+
+/* dlogits (type and ld of logits; may be logits itself, else no overlap), for
+ * the upstream gradients dlogp and dentropy ([rows] fp32, either may be NULL,
+ * not both):
+ *   dx_v = dlogp (1[v = target] - p_v) - dentropy p_v (ln p_v + entropy)
+ * stats, and entropy when dentropy is given, are the forward's.  dlogp needs
+ * target; a row whose target is negative (or >= vocab, which also sets bit 2
+ * of the device error word) takes dlogp = 0.  A row whose two gradients are
+ * both 0 gets exact zeros without reading its logits; a row of -inf alone gets
+ * zeros; a row with +inf or NaN gets NaN.  Columns from vocab to ld are not
+ * touched. */
+int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, int logits_f32,
+                           const void *logits, const int *target, const float *stats,
+                           const float *entropy, const float *dlogp, const float *dentropy,
+                           void *dlogits, gptl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,7 +42,14 @@ enum {
   GPTL_KIND_ATTN_BWD = 14,   /* fused causal attention backward (dQ; dK, dV)  */
   GPTL_KIND_CLIP = 15,       /* global-norm clip coefficient (one block)      */
   GPTL_KIND_ACCUMULATE = 16, /* gradient accumulation acc += grad             */
-  GPTL_KIND_COUNT = 17
+  GPTL_KIND_QK_ROPE_FWD = 17, /* norm and rotation of queries and keys        */
+  GPTL_KIND_QK_ROPE_BWD = 18, /* its backward (rows pass)                     */
+  GPTL_KIND_DROPOUT_FWD = 19, /* bias + dropout + residual                    */
+  GPTL_KIND_DROPOUT_BWD = 20, /* its backward                                 */
+  GPTL_KIND_RNG = 21,         /* dropout state advance (one thread)           */
+  GPTL_KIND_LOGPROB_FWD = 22, /* token log probability, entropy, top          */
+  GPTL_KIND_LOGPROB_BWD = 23, /* its gradient                                 */
+  GPTL_KIND_COUNT = 24
 };
 
 /* step tags */

@@ -23,6 +23,8 @@ Modules:
           stack_fwd / stack_bwd (layers of one shape, chained)
   optim   found_inf, adam_step, loss_scale_update, cast_to_16, grad_norm,
           clip_coefficient, accumulate
+  parts   the parts around the layer (no counterpart on the pages): norm and
+          rotation of queries and keys, dropout, token log probabilities
 
 Parity status: every function is pinned by tests in tests/test_oracle_*.py
 (finite differences, sharded == unsharded, closed forms, hand-computed
@@ -36,9 +38,10 @@ from .layer import (layer_fwd, layer_bwd, layer_norm_fwd, layer_norm_bwd, gelu,
                     stack_fwd, stack_bwd, STORE_POINTS)
 from .optim import (found_inf, adam_step, loss_scale_update, cast_to_16, grad_norm,
                     clip_coefficient, accumulate)
+from . import parts
 
 __all__ = ["layer_fwd", "layer_bwd", "stack_fwd", "stack_bwd", "layer_norm_fwd", "layer_norm_bwd", "gelu",
            "gelu_prime", "causal_softmax", "attention_head_fwd", "attention_head_bwd",
            "STORE_POINTS", "found_inf",
            "adam_step", "loss_scale_update", "cast_to_16", "grad_norm", "clip_coefficient",
-           "accumulate"]
+           "accumulate", "parts"]

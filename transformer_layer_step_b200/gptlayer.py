@@ -71,13 +71,25 @@ class GemmDesc(C.Structure):
                 ("ws_bytes", C.c_longlong), ("colsum", C.c_void_p)]
 
 
+class QkDesc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("tokens", "groups", "q_heads", "k_heads", "v_heads",
+                                       "head_dim", "rot_dim", "interleaved", "axes", "seq")] + \
+               [("eps", C.c_float)] + \
+               [(n, C.c_longlong) for n in ("x_ld", "x_gstride", "y_ld", "y_gstride")]
+
+
+class RopePair(C.Structure):
+    _fields_ = [("turns", C.c_double), ("axis", C.c_int), ("reserved", C.c_int)]
+
+
 class LaunchRecord(C.Structure):
     _fields_ = [("kind", C.c_int), ("tag", C.c_int), ("ms", C.c_float)]
 
 
 KIND_NAMES = ("gemm", "ln_fwd", "ln_bwd", "reserved3", "reserved4", "colsum", "reduce",
               "overflow", "adam", "scale", "splitk", "attn_fwd", "rowdot", "transpose", "attn_bwd",
-              "clip", "accumulate")
+              "clip", "accumulate", "qk_rope_fwd", "qk_rope_bwd", "dropout_fwd", "dropout_bwd", "rng",
+              "logprob_fwd", "logprob_bwd")
 
 _lib = None
 
@@ -137,6 +149,22 @@ _SIGS = {
     "gptl_attention_bwd": (C.c_int, [C.c_int] * 6 + [C.c_void_p] * 9),
     "gptl_colsum_noalloc": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_longlong, C.c_longlong,
                                       C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "gptl_rope_table": (C.c_int, [C.c_int, C.c_int, C.POINTER(C.c_int), C.c_int, C.c_double,
+                                  C.POINTER(RopePair)]),
+    "gptl_qk_norm_rope_fwd": (C.c_int, [C.POINTER(QkDesc), C.c_int] + [C.c_void_p] * 7),
+    "gptl_qk_norm_rope_scratch_bytes": (C.c_size_t, [C.POINTER(QkDesc)]),
+    "gptl_qk_norm_rope_bwd": (C.c_int, [C.POINTER(QkDesc), C.c_int] + [C.c_void_p] * 11),
+    "gptl_rng_advance": (C.c_int, [C.c_void_p, C.c_ulonglong, C.c_void_p]),
+    "gptl_dropout_add_fwd": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                       C.c_void_p, C.c_int, C.c_float, C.c_void_p, C.c_uint,
+                                       C.c_void_p, C.c_int, C.c_void_p]),
+    "gptl_dropout_scratch_bytes": (C.c_size_t, [C.c_int, C.c_int]),
+    "gptl_dropout_add_bwd": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_float,
+                                       C.c_void_p, C.c_uint] + [C.c_void_p] * 4),
+    "gptl_token_logprob_fwd": (C.c_int, [C.c_int, C.c_int, C.c_longlong, C.c_int, C.c_int] +
+                               [C.c_void_p] * 5 + [C.c_int] + [C.c_void_p] * 3),
+    "gptl_token_logprob_bwd": (C.c_int, [C.c_int, C.c_int, C.c_longlong, C.c_int, C.c_int] +
+                               [C.c_void_p] * 8),
     "gptl_launch_count": (C.c_ulonglong, []),
     "gptl_profile_begin": (C.c_int, [C.c_int]),
     "gptl_profile_end": (C.c_int, [C.POINTER(LaunchRecord), C.c_int, C.POINTER(C.c_int),
@@ -385,6 +413,85 @@ def colsum_noalloc(rows, n, groups, ld, gstride, dtype, a, out, stream=0):
     """gptl_colsum without caller scratch (fixed library array; see the header)."""
     _check(lib().gptl_colsum_noalloc(rows, n, groups, ld, gstride, DTYPES.get(dtype, dtype),
                                      _ptr(a), _ptr(out), stream), "gptl_colsum_noalloc")
+
+
+def make_qk_desc(tokens, groups, q_heads, k_heads, v_heads, head_dim, rot_dim, interleaved=0, axes=1,
+                 seq=0, eps=1e-6, x_ld=0, x_gstride=0, y_ld=0, y_gstride=0) -> QkDesc:
+    """Sizes of the packed rows of qk_norm_rope_fwd / _bwd (0 strides: dense)."""
+    return QkDesc(tokens, groups, q_heads, k_heads, v_heads, head_dim, rot_dim, int(interleaved),
+                  axes, seq, eps, x_ld, x_gstride, y_ld, y_gstride)
+
+
+def rope_table(rot_dim, base=10000.0, axis_pairs=None, per_axis=False):
+    """gptl_rope_table's host array (a ctypes array of RopePair; copy its bytes
+    to the device).  axis_pairs: pairs of each axis, default one axis."""
+    pairs = [rot_dim // 2] if axis_pairs is None else list(axis_pairs)
+    table = (RopePair * max(rot_dim // 2, 1))()
+    _check(lib().gptl_rope_table(rot_dim, len(pairs), (C.c_int * len(pairs))(*pairs),
+                                 int(per_axis), base, table), "gptl_rope_table")
+    return table
+
+
+def qk_norm_rope_fwd(desc: QkDesc, dtype, x, y, gq, gk, pos, table, stream=0):
+    _check(lib().gptl_qk_norm_rope_fwd(C.byref(desc), DTYPES.get(dtype, dtype), _ptr(x), _ptr(y),
+                                       _ptr(gq), _ptr(gk), _ptr(pos), _ptr(table), stream),
+           "gptl_qk_norm_rope_fwd")
+
+
+def qk_norm_rope_scratch_bytes(desc: QkDesc) -> int:
+    return lib().gptl_qk_norm_rope_scratch_bytes(C.byref(desc))
+
+
+def qk_norm_rope_bwd(desc: QkDesc, dtype, x, dy, dx, gq, gk, pos, table, dgq, dgk, scratch,
+                     stream=0):
+    _check(lib().gptl_qk_norm_rope_bwd(C.byref(desc), DTYPES.get(dtype, dtype), _ptr(x), _ptr(dy),
+                                       _ptr(dx), _ptr(gq), _ptr(gk), _ptr(pos), _ptr(table),
+                                       _ptr(dgq), _ptr(dgk), _ptr(scratch), stream),
+           "gptl_qk_norm_rope_bwd")
+
+
+def rng_advance(rng, n, stream=0):
+    """rng.offset += n on the device (rng: two 64-bit words, seed and offset)."""
+    _check(lib().gptl_rng_advance(_ptr(rng), n, stream), "gptl_rng_advance")
+
+
+def dropout_add_fwd(rows, h, dtype, x, bias, resid, resid_f32, p, rng, site, y, y_f32, stream=0):
+    _check(lib().gptl_dropout_add_fwd(rows, h, DTYPES.get(dtype, dtype), _ptr(x), _ptr(bias),
+                                      _ptr(resid), int(resid_f32), p, _ptr(rng), site, _ptr(y),
+                                      int(y_f32), stream), "gptl_dropout_add_fwd")
+
+
+def dropout_scratch_bytes(rows, h) -> int:
+    return lib().gptl_dropout_scratch_bytes(rows, h)
+
+
+def dropout_add_bwd(rows, h, dtype, dy, dy_f32, p, rng, site, dx, dbias=None, scratch=None,
+                    stream=0):
+    _check(lib().gptl_dropout_add_bwd(rows, h, DTYPES.get(dtype, dtype), _ptr(dy), int(dy_f32), p,
+                                      _ptr(rng), site, _ptr(dx), _ptr(dbias), _ptr(scratch),
+                                      stream), "gptl_dropout_add_bwd")
+
+
+# logits types of token_logprob_fwd / _bwd: (gptl_dtype, logits_f32)
+LOGIT_TYPES = {"fp16": (FP16, 0), "bf16": (BF16, 0), "fp32": (BF16, 1)}
+
+
+def token_logprob_fwd(rows, vocab, ld, dtype, logits, target, logp, entropy=None, stats=None,
+                      top_k=0, top_logp=None, top_id=None, stream=0):
+    """dtype: the logits' type, "fp16", "bf16" or "fp32"."""
+    dt, f32 = LOGIT_TYPES[dtype]
+    _check(lib().gptl_token_logprob_fwd(rows, vocab, ld, dt, f32, _ptr(logits), _ptr(target),
+                                        _ptr(logp), _ptr(entropy), _ptr(stats), top_k,
+                                        _ptr(top_logp), _ptr(top_id), stream),
+           "gptl_token_logprob_fwd")
+
+
+def token_logprob_bwd(rows, vocab, ld, dtype, logits, target, stats, entropy, dlogp, dentropy,
+                      dlogits, stream=0):
+    dt, f32 = LOGIT_TYPES[dtype]
+    _check(lib().gptl_token_logprob_bwd(rows, vocab, ld, dt, f32, _ptr(logits), _ptr(target),
+                                        _ptr(stats), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
+                                        _ptr(dlogits), stream), "gptl_token_logprob_bwd")
 
 
 def read_device_error(clear: bool = True) -> int:
