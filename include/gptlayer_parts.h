@@ -207,7 +207,8 @@ int gptl_colsum_noalloc(int rows, int n, int groups, long long ld, long long gst
  * (exact to fp32 for every int position), and y is rounded once.
  * interleaved = 0 pairs elements (j, j + rot_dim/2), 1 pairs (2j, 2j + 1). */
 typedef struct {
-  int tokens, groups;              /* rows of each group, groups (tp shards)  */
+  int tokens, groups;              /* rows of a group, groups (tp shards);    */
+                                   /* tokens * groups < 2^30                  */
   int q_heads, k_heads, v_heads;   /* of one group; v_heads may be 0          */
   int head_dim;                    /* multiple of 16, at most 256             */
   int rot_dim;                     /* multiple of 16, 0 .. head_dim           */

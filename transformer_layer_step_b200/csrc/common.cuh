@@ -313,6 +313,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return u;
 }
 
+// Two fp32 operations in one instruction (each half rounded to nearest, as the
+// scalar ones are).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
 // Single-instruction base-2 exponential and reciprocal of the SFU
 // (ex2.approx / rcp.approx, flush-to-zero): relative error about 2^-22.
 __device__ __forceinline__ float ex2_approx(float x) {

@@ -24,40 +24,37 @@
 namespace gptl {
 
 constexpr int kQkWarps = 8;             // warps of a block
-constexpr int kQkMaxPairs = 128;        // head_dim <= 256
 constexpr int kQkMaxBlocks = 592;       // partial rows of the gains' gradients
+constexpr int kQkFwdBlocks = 4, kQkBwdBlocks = 2;              // resident on an SM
+constexpr double kQkFwdAngles = 4.0, kQkBwdAngles = 2.0;       // a token's angles, in slots
+
+// The heads of one kind.  A slot is a warp's step: 32/LPH neighbouring heads of
+// one group.  A chunk is `spc` slots of the groups * slots of a token.
+struct QkKind {
+  int heads, first;                     // heads of a group, the first one's place in the row
+  int slots, chunks, spc;
+  int warps;                            // warps of one chunk: they share its tokens
+};
 
 struct QkParams {
   const void *x, *dy;
   void *out;
-  const void *gq, *gk;
+  const void *gain[2];
   const int *pos;
   const gptl_rope_pair *table;
-  float *part;                          // [2][gridDim.x][hd] (backward with gains)
+  float *part;                          // partial sums: queries' blocks, then keys', [hd] each
   long long x_ld, x_gs, y_ld, y_gs;
-  unsigned items, chunks, spc;          // (token, chunk of head slots) pairs; q, k slots per chunk
-  int tokens, q, k, v, hd, rot, axes, seq, interleaved;
-  int slots_q, slots_k, slots_v;        // groups of 32/LPH heads of each kind
+  QkKind kind[2];                       // queries, keys
+  int blocks_q, blocks_qk;              // blocks [0, blocks_q), [blocks_q, blocks_qk), then values
+  int v_vecs, v_first, v_blocks;        // 16-byte vectors of a row's values, the first's place
+  int tokens, groups, hd, rot, axes, seq;
   float eps, inv_hd;
 };
 
-// The 16 elements of a lane within its head: two vectors of 8 at v0 and v1.
-struct QkLane {
-  int sub, v0, v1;
-  bool on, turns;
-  __device__ QkLane(const QkParams &p, int lane, int lph) {
-    const int c = lane % lph;
-    sub = lane / lph;
-    on = c < p.hd / 16;
-    turns = c < p.rot / 16;
-    const bool split = turns && !p.interleaved;       // partners rot/2 apart
-    v0 = split ? 8 * c : 16 * c;
-    v1 = split ? v0 + p.rot / 2 : v0 + 8;
-  }
-};
-
-// Sines and cosines of one token's pairs, by the whole warp.
-__device__ __forceinline__ void qk_angles(const QkParams &p, int token, float2 *cs, int lane) {
+// Sines and cosines of one token's pairs, by the whole warp.  Lane c of a head
+// holds pairs 8c .. 8c + 7; cs[i * lanes + c] = cosines of its pairs 2i and 2i + 1,
+// then their sines, so that the lanes of a head read 16 neighbouring bytes each.
+__device__ __forceinline__ void qk_angles(const QkParams &p, int token, float4 *cs, int lanes, int lane) {
   __syncwarp();
   for (int j = lane; j < p.rot / 2; j += 32) {
     const gptl_rope_pair e = p.table[j];
@@ -71,276 +68,288 @@ __device__ __forceinline__ void qk_angles(const QkParams &p, int token, float2 *
     t -= rint(t);
     float s, c;
     sincospif(2.0f * (float)t, &s, &c);
-    cs[j] = make_float2(c, s);
+    float *to = reinterpret_cast<float *>(cs + (j % 8 / 2) * lanes + j / 8) + j % 2;
+    to[0] = c;
+    to[2] = s;
   }
   __syncwarp();
 }
 
-// Turns the pairs held in a, b (vectors v0 and v1) by (cos, dir * sin).
-__device__ __forceinline__ void qk_turn(float (&a)[8], float (&b)[8], const float2 (&cs)[8],
-                                        bool interleaved, float dir) {
-  if (interleaved) {
+// A lane's 8 pairs (a, b): v0 and v1 hold them as neighbours (INTER) or as the
+// vectors of first and of second elements.
+template <typename T, bool INTER>
+__device__ __forceinline__ void qk_unpack(const uint4 &v0, const uint4 &v1, float (&a)[8],
+                                          float (&b)[8]) {
+  if constexpr (INTER) {
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c0 = cs[i].x, s0 = dir * cs[i].y, c1 = cs[4 + i].x, s1 = dir * cs[4 + i].y;
-      const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
-      a[2 * i] = x0 * c0 - y0 * s0;
-      a[2 * i + 1] = y0 * c0 + x0 * s0;
-      b[2 * i] = x1 * c1 - y1 * s1;
-      b[2 * i + 1] = y1 * c1 + x1 * s1;
+    for (int i = 0; i < 8; ++i) {
+      const float2 q = Cvt<T>::unpack2(w[i]);
+      a[i] = q.x;
+      b[i] = q.y;
     }
   } else {
+    unpack8<T>(v0, a);
+    unpack8<T>(v1, b);
+  }
+}
+template <typename T, bool INTER>
+__device__ __forceinline__ void qk_pack(const float (&a)[8], const float (&b)[8], uint4 &v0, uint4 &v1) {
+  if constexpr (INTER) {
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = cs[i].x, s = dir * cs[i].y;
-      const float x = a[i], y = b[i];
-      a[i] = x * c - y * s;
-      b[i] = y * c + x * s;
+    for (int i = 0; i < 8; ++i) w[i] = Cvt<T>::pack2(a[i], b[i]);
+    v0 = make_uint4(w[0], w[1], w[2], w[3]);
+    v1 = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    v0 = pack8<T>(a);
+    v1 = pack8<T>(b);
+  }
+}
+
+// Turns the pairs (a, b) by (cos, dir * sin) of the lane's table entries.
+__device__ __forceinline__ void qk_turn(float (&a)[8], float (&b)[8], const float4 *cs, int lanes,
+                                        float dir) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 q = cs[i * lanes];
+    const float c[2] = {q.x, q.y}, s[2] = {dir * q.z, dir * q.w};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = a[2 * i + e], y = b[2 * i + e];
+      a[2 * i + e] = fmaf(x, c[e], -(y * s[e]));
+      b[2 * i + e] = fmaf(y, c[e], x * s[e]);
     }
   }
 }
 
-// Column of the first element of a lane's head in slot s (queries, then keys),
-// or -1 for no head.  Heads of a kind fill their slots in order, 32/LPH to a slot.
-__device__ __forceinline__ int qk_column(const QkParams &p, int s, int hpw, const QkLane &L) {
-  const bool key = s >= p.slots_q;
-  const int h = (key ? s - p.slots_q : s) * hpw + L.sub;
-  return L.on && h < (key ? p.k : p.q) ? (key ? p.q + h : h) * p.hd : -1;
-}
-
-// Copies chunk `chunk`'s share of a row's value heads.
+// The value heads of the last blocks: a warp copies every v_warps-th row.
 template <typename T>
-__device__ __forceinline__ void qk_copy_values(const QkParams &p, unsigned chunk, int hpw,
-                                               const QkLane &L, const T *from, T *to) {
-  const int lo = (int)((long long)p.slots_v * chunk / p.chunks);
-  const int hi = (int)((long long)p.slots_v * (chunk + 1) / p.chunks);
-#pragma unroll 2
-  for (int s = lo; s < hi; ++s) {
-    const int h = s * hpw + L.sub;
-    if (!L.on || h >= p.v) continue;
-    const long long col = (long long)(p.q + p.k + h) * p.hd;
-    const uint4 a = *reinterpret_cast<const uint4 *>(from + col + L.v0);
-    const uint4 b = *reinterpret_cast<const uint4 *>(from + col + L.v1);
-    *reinterpret_cast<uint4 *>(to + col + L.v0) = a;
-    *reinterpret_cast<uint4 *>(to + col + L.v1) = b;
+__device__ void qk_copy_values(const QkParams &p, const T *from, long long f_ld, long long f_gs, T *to) {
+  const int lane = threadIdx.x & 31;
+  const unsigned warps = p.v_blocks * kQkWarps;
+  const unsigned rows = (unsigned)p.tokens * p.groups;
+  for (unsigned r = (blockIdx.x - p.blocks_qk) * kQkWarps + threadIdx.x / 32; r < rows; r += warps) {
+    const unsigned g = r / p.tokens, t = r - g * p.tokens;
+    const uint4 *src = reinterpret_cast<const uint4 *>(from + g * f_gs + t * f_ld) + p.v_first;
+    uint4 *dst = reinterpret_cast<uint4 *>(to + g * p.y_gs + t * p.y_ld) + p.v_first;
+    int i = lane;
+    for (; i + 96 < p.v_vecs; i += 128) {
+      const uint4 a = src[i], b = src[i + 32], c = src[i + 64], d = src[i + 96];
+      dst[i] = a; dst[i + 32] = b; dst[i + 64] = c; dst[i + 96] = d;
+    }
+    for (; i < p.v_vecs; i += 32) dst[i] = src[i];
   }
 }
 
-// Gains of queries and keys in shared memory, fp32 (1 where there are none).
-template <typename T>
-__device__ __forceinline__ void qk_gains(const QkParams &p, float *gain) {
-  for (int i = threadIdx.x; i < p.hd; i += blockDim.x) {
-    gain[i] = p.gq ? Cvt<T>::to_f(static_cast<const T *>(p.gq)[i]) : 1.f;
-    gain[p.hd + i] = p.gk ? Cvt<T>::to_f(static_cast<const T *>(p.gk)[i]) : 1.f;
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ void qk_load_gain(const float *g, const QkLane &L, float (&a)[8],
-                                             float (&b)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 u = *reinterpret_cast<const float4 *>(g + L.v0 + i);
-    const float4 w = *reinterpret_cast<const float4 *>(g + L.v1 + i);
-    a[i] = u.x; a[i + 1] = u.y; a[i + 2] = u.z; a[i + 3] = u.w;
-    b[i] = w.x; b[i + 1] = w.y; b[i + 2] = w.z; b[i + 3] = w.w;
-  }
-}
-
-template <typename T, int LPH>
-__global__ void __launch_bounds__(kQkWarps * 32, 3) qk_rope_fwd_kernel(const QkParams p) {
+// BWD: out = dx from x and dy; else out = y from x.  NORM: with gains.
+template <typename T, int LPH, bool INTER, bool NORM, bool BWD>
+__global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBlocks)
+    qk_rope_kernel(const QkParams p) {
   constexpr int HPW = 32 / LPH;
-  __shared__ __align__(16) float2 cs_all[kQkWarps][kQkMaxPairs];
-  __shared__ __align__(16) float gain[512];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const QkLane L(p, lane, LPH);
-  const bool norm = p.gq != nullptr;
-  if (norm) qk_gains<T>(p, gain);
-  for (unsigned item = blockIdx.x * kQkWarps + warp; item < p.items; item += gridDim.x * kQkWarps) {
-    const unsigned row = item / p.chunks, chunk = item - row * p.chunks;
-    const unsigned g = row / p.tokens, token = row - g * p.tokens;
-    const T *x = static_cast<const T *>(p.x) + g * p.x_gs + token * p.x_ld;
-    T *y = static_cast<T *>(p.out) + g * p.y_gs + token * p.y_ld;
-    const int s0 = chunk * p.spc, s1 = min(s0 + (int)p.spc, p.slots_q + p.slots_k);
-    uint4 n0 = {}, n1 = {};
-    int ncol = qk_column(p, s0, HPW, L);
-    if (ncol >= 0) {
-      n0 = *reinterpret_cast<const uint4 *>(x + ncol + L.v0);
-      n1 = *reinterpret_cast<const uint4 *>(x + ncol + L.v1);
-    }
-    float2 cs[8];
-    if (p.rot) {
-      qk_angles(p, token, cs_all[warp], lane);
-      if (L.turns) {
-        const float4 *src = reinterpret_cast<const float4 *>(cs_all[warp] + 8 * (lane % LPH));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 u = src[i];
-          cs[2 * i] = make_float2(u.x, u.y);
-          cs[2 * i + 1] = make_float2(u.z, u.w);
-        }
-      }
-    }
-    for (int s = s0; s < s1; ++s) {
-      const uint4 u0 = n0, u1 = n1;
-      const int col = ncol;
-      if (s + 1 < s1) {                          // the next slot's loads go out first
-        ncol = qk_column(p, s + 1, HPW, L);
-        n0 = n1 = uint4{};
-        if (ncol >= 0) {
-          n0 = *reinterpret_cast<const uint4 *>(x + ncol + L.v0);
-          n1 = *reinterpret_cast<const uint4 *>(x + ncol + L.v1);
-        }
-      }
-      float a[8], b[8];
-      unpack8<T>(u0, a);
-      unpack8<T>(u1, b);
-      if (norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-        if (col >= 0) {
-          float ga[8], gb[8];
-          qk_load_gain(gain + (s < p.slots_q ? 0 : p.hd), L, ga, gb);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            a[i] = a[i] * r * ga[i];
-            b[i] = b[i] * r * gb[i];
-          }
-        }
-      }
-      if (col < 0) continue;
-      if (L.turns) qk_turn(a, b, cs, p.interleaved, 1.f);
-      *reinterpret_cast<uint4 *>(y + col + L.v0) = pack8<T>(a);
-      *reinterpret_cast<uint4 *>(y + col + L.v1) = pack8<T>(b);
-    }
-    if (p.slots_v) qk_copy_values<T>(p, chunk, HPW, L, x, y);
+  constexpr bool kX = NORM || !BWD;                        // x is read
+  __shared__ __align__(16) float4 cs_all[kQkWarps][4 * LPH];
+  __shared__ __align__(16) float4 gain_all[NORM ? 4 * LPH : 1];   // as cs_all: (a, a, b, b)
+  __shared__ float sums[BWD && NORM ? kQkWarps : 1][256];
+  const T *in_x = static_cast<const T *>(p.x), *in_dy = static_cast<const T *>(p.dy);
+  T *out = static_cast<T *>(p.out);
+  if ((int)blockIdx.x >= p.blocks_qk) {
+    if constexpr (BWD) qk_copy_values<T>(p, in_dy, p.y_ld, p.y_gs, out);
+    else qk_copy_values<T>(p, in_x, p.x_ld, p.x_gs, out);
+    return;
   }
-}
-
-template <typename T, int LPH>
-__global__ void __launch_bounds__(kQkWarps * 32, 2) qk_rope_bwd_kernel(const QkParams p) {
-  constexpr int HPW = 32 / LPH;
-  __shared__ __align__(16) float2 cs_all[kQkWarps][kQkMaxPairs];
-  __shared__ __align__(16) float gain[512];
-  __shared__ float sums[kQkWarps][512];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const QkLane L(p, lane, LPH);
-  const bool norm = p.gq != nullptr;
-  if (norm) qk_gains<T>(p, gain);
-  float dq0[8] = {}, dq1[8] = {}, dk0[8] = {}, dk1[8] = {};
-  for (unsigned item = blockIdx.x * kQkWarps + warp; item < p.items; item += gridDim.x * kQkWarps) {
-    const unsigned row = item / p.chunks, chunk = item - row * p.chunks;
-    const unsigned g = row / p.tokens, token = row - g * p.tokens;
-    const T *x = static_cast<const T *>(p.x) + g * p.x_gs + token * p.x_ld;
-    const T *dy = static_cast<const T *>(p.dy) + g * p.y_gs + token * p.y_ld;
-    T *dx = static_cast<T *>(p.out) + g * p.y_gs + token * p.y_ld;
-    const int s0 = chunk * p.spc, s1 = min(s0 + (int)p.spc, p.slots_q + p.slots_k);
-    float2 cs[8];
-    if (p.rot) {
-      qk_angles(p, token, cs_all[warp], lane);
-      if (L.turns) {
-        const float4 *src = reinterpret_cast<const float4 *>(cs_all[warp] + 8 * (lane % LPH));
+  const bool key = (int)blockIdx.x >= p.blocks_q;
+  const QkKind &K = p.kind[key];
+  const int w = ((int)blockIdx.x - (key ? p.blocks_q : 0)) * kQkWarps + warp;
+
+  // the lane's 16 elements of a head: two vectors of 8 at v0 and v1
+  const int c = lane % LPH, sub = lane / LPH;
+  const bool on = c < p.hd / 16, turns = c < p.rot / 16;
+  const bool split = turns && !INTER;                      // partners rot/2 apart
+  const int v0 = !on ? 0 : split ? 8 * c : 16 * c, v1 = split ? v0 + p.rot / 2 : v0 + 8;
+
+  if constexpr (NORM) {
+    if (warp == 0 && lane < LPH) {
+      const T *g = static_cast<const T *>(p.gain[key]);
+      float ga[8] = {}, gb[8] = {};                        // 0 beyond the head's elements
+      if (on)
+        qk_unpack<T, INTER>(*reinterpret_cast<const uint4 *>(g + v0),
+                            *reinterpret_cast<const uint4 *>(g + v1), ga, gb);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 u = src[i];
-          cs[2 * i] = make_float2(u.x, u.y);
-          cs[2 * i + 1] = make_float2(u.z, u.w);
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        gain_all[i * LPH + c] = make_float4(ga[2 * i], ga[2 * i + 1], gb[2 * i], gb[2 * i + 1]);
     }
-    // the slots [lo, hi) of one kind of head, its gain's gradient in (acc0, acc1)
-    auto heads = [&](int lo, int hi, const float *gp, float (&acc0)[8], float (&acc1)[8]) {
-      uint4 nx0 = {}, nx1 = {}, nd0 = {}, nd1 = {};
-      int ncol = -1;
-      auto fetch = [&](int s) {
-        ncol = qk_column(p, s, HPW, L);
+    __syncthreads();
+  }
+  const float4 *gain = gain_all + c, *cs = cs_all[warp] + c;
+  float acc_a[8] = {}, acc_b[8] = {};                      // the gain's gradient
+
+  const int chunk = w / K.warps;
+  const int u0 = chunk * K.spc, n_slots = min(K.spc, p.groups * K.slots - u0);
+  const int g0 = u0 / K.slots, s0 = u0 - g0 * K.slots;
+  const int step = HPW * p.hd, dv = v1 - v0;
+  const long long col = (long long)s0 * step + (K.first + sub) * p.hd + v0;
+  const long long x_wrap = p.x_gs - (long long)K.slots * step, y_wrap = p.y_gs - (long long)K.slots * step;
+  const int h_last = on ? K.heads - sub : 0;               // a head in slot s where s * HPW < h_last
+  for (int token = chunk < K.chunks ? w - chunk * K.warps : p.tokens; token < p.tokens;
+       token += K.warps) {
+    // the next slot to fetch: its number within the group, its places
+    int hs = s0 * HPW;
+    const T *px = in_x + g0 * p.x_gs + token * p.x_ld + col;
+    const T *pd = in_dy + g0 * p.y_gs + token * p.y_ld + col;
+    T *po = out + g0 * p.y_gs + token * p.y_ld + col, *o = po;
+    uint4 nx0, nx1, nd0, nd1;
+    bool live, here;
+    auto fetch = [&]() {
+      live = hs < h_last;
+      o = po;
+      if (live) {
+        if constexpr (kX) {
+          nx0 = *reinterpret_cast<const uint4 *>(px);
+          nx1 = *reinterpret_cast<const uint4 *>(px + dv);
+        }
+        if constexpr (BWD) {
+          nd0 = *reinterpret_cast<const uint4 *>(pd);
+          nd1 = *reinterpret_cast<const uint4 *>(pd + dv);
+        }
+      } else {
         nx0 = nx1 = nd0 = nd1 = uint4{};
-        if (ncol < 0) return;
-        nd0 = *reinterpret_cast<const uint4 *>(dy + ncol + L.v0);
-        nd1 = *reinterpret_cast<const uint4 *>(dy + ncol + L.v1);
-        if (norm) {
-          nx0 = *reinterpret_cast<const uint4 *>(x + ncol + L.v0);
-          nx1 = *reinterpret_cast<const uint4 *>(x + ncol + L.v1);
-        }
-      };
-      if (lo < hi) fetch(lo);
-      for (int s = lo; s < hi; ++s) {
-        const uint4 x0 = nx0, x1 = nx1, d0 = nd0, d1 = nd1;
-        const int col = ncol;
-        if (s + 1 < hi) fetch(s + 1);
-        float a[8], b[8];
-        unpack8<T>(d0, a);
-        unpack8<T>(d1, b);
-        if (L.turns) qk_turn(a, b, cs, p.interleaved, -1.f);
-        if (norm) {
-          float xa[8], xb[8], ga[8], gb[8], ss = 0.f, sd = 0.f;
-          unpack8<T>(x0, xa);
-          unpack8<T>(x1, xb);
-          if (L.on) {
-            qk_load_gain(gp, L, ga, gb);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ga[i] = gb[i] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-            sd = fmaf(a[i] * ga[i], xa[i], fmaf(b[i] * gb[i], xb[i], sd));
-          }
-#pragma unroll
-          for (int o = LPH / 2; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            sd += __shfl_xor_sync(0xffffffffu, sd, o);
-          }
-          const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-          const float w = r * r * r * (sd * p.inv_hd);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc0[i] = fmaf(a[i], xa[i] * r, acc0[i]);
-            acc1[i] = fmaf(b[i], xb[i] * r, acc1[i]);
-            a[i] = r * (a[i] * ga[i]) - w * xa[i];
-            b[i] = r * (b[i] * gb[i]) - w * xb[i];
-          }
-        }
-        if (col < 0) continue;
-        *reinterpret_cast<uint4 *>(dx + col + L.v0) = pack8<T>(a);
-        *reinterpret_cast<uint4 *>(dx + col + L.v1) = pack8<T>(b);
+      }
+      hs += HPW;
+      px += step;
+      pd += step;
+      po += step;
+      if (hs >= K.heads) {
+        hs = 0;
+        px += x_wrap;
+        pd += y_wrap;
+        po += y_wrap;
       }
     };
-    heads(s0, min(s1, p.slots_q), gain, dq0, dq1);
-    heads(max(s0, p.slots_q), s1, gain + p.hd, dk0, dk1);
-    if (p.slots_v) qk_copy_values<T>(p, chunk, HPW, L, dy, dx);
+    fetch();
+    if (p.rot) qk_angles(p, token, cs_all[warp], LPH, lane);
+    for (int u = 0; u < n_slots; ++u) {
+      {
+        const uint4 x0 = nx0, x1 = nx1, d0 = nd0, d1 = nd1;
+        T *to = o;
+        here = live;
+        if (u + 1 < n_slots) fetch();                      // the next slot's loads go out first
+        float a[8], b[8];
+        if constexpr (BWD) {
+          qk_unpack<T, INTER>(d0, d1, a, b);
+          if (turns) qk_turn(a, b, cs, LPH, -1.f);
+        }
+        if constexpr (NORM) {
+          float xa[8], xb[8], ss = 0.f, sd = 0.f;
+          qk_unpack<T, INTER>(x0, x1, xa, xb);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+          if constexpr (BWD) {
+            // the gain's gradient takes dn x, then dn becomes d = dn g
+            float ta[8], tb[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 g = gain[i * LPH];
+              const float ga[2] = {g.x, g.y}, gb[2] = {g.z, g.w};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int k = 2 * i + e;
+                ta[k] = a[k] * xa[k];
+                tb[k] = b[k] * xb[k];
+                sd = fmaf(ta[k], ga[e], fmaf(tb[k], gb[e], sd));
+                a[k] *= ga[e];
+                b[k] *= gb[e];
+              }
+            }
+#pragma unroll
+            for (int o2 = LPH / 2; o2 > 0; o2 >>= 1) {
+              ss += __shfl_xor_sync(0xffffffffu, ss, o2);
+              sd += __shfl_xor_sync(0xffffffffu, sd, o2);
+            }
+            const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+            const float m = -r * r * r * (sd * p.inv_hd);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              acc_a[k] = fmaf(ta[k], r, acc_a[k]);
+              acc_b[k] = fmaf(tb[k], r, acc_b[k]);
+              a[k] = fmaf(a[k], r, xa[k] * m);
+              b[k] = fmaf(b[k], r, xb[k] * m);
+            }
+          } else {
+#pragma unroll
+            for (int o2 = LPH / 2; o2 > 0; o2 >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o2);
+            const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 g = gain[i * LPH];
+              a[2 * i] = xa[2 * i] * r * g.x;
+              a[2 * i + 1] = xa[2 * i + 1] * r * g.y;
+              b[2 * i] = xb[2 * i] * r * g.z;
+              b[2 * i + 1] = xb[2 * i + 1] * r * g.w;
+            }
+          }
+        } else if constexpr (!BWD) {
+          qk_unpack<T, INTER>(x0, x1, a, b);
+        }
+        if (!BWD && turns) qk_turn(a, b, cs, LPH, 1.f);
+        if (here) {
+          uint4 q0, q1;
+          qk_pack<T, INTER>(a, b, q0, q1);
+          *reinterpret_cast<uint4 *>(to) = q0;
+          *reinterpret_cast<uint4 *>(to + dv) = q1;
+        }
+      }
+    }
   }
-  if (!norm) return;
-  // the warp's head positions, then the block's warps, each in a fixed order
+  if constexpr (BWD && NORM) {
+    // the warp's head positions, then the block's warps, each in a fixed order
+    float f[16];
 #pragma unroll
-  for (int o = LPH; o < 32; o <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dq0[i] += __shfl_xor_sync(0xffffffffu, dq0[i], o);
-      dq1[i] += __shfl_xor_sync(0xffffffffu, dq1[i], o);
-      dk0[i] += __shfl_xor_sync(0xffffffffu, dk0[i], o);
-      dk1[i] += __shfl_xor_sync(0xffffffffu, dk1[i], o);
+    for (int i = 0; i < 8; ++i) {                          // in the order of v0 and v1
+      f[INTER ? 2 * i : i] = acc_a[i];
+      f[INTER ? 2 * i + 1 : 8 + i] = acc_b[i];
     }
-  if (lane < LPH && L.on)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sums[warp][L.v0 + i] = dq0[i];
-      sums[warp][L.v1 + i] = dq1[i];
-      sums[warp][p.hd + L.v0 + i] = dk0[i];
-      sums[warp][p.hd + L.v1 + i] = dk1[i];
+    for (int o = LPH; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] += __shfl_xor_sync(0xffffffffu, f[i], o);
+    if (lane < LPH && on)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sums[warp][v0 + i] = f[i];
+        sums[warp][v1 + i] = f[8 + i];
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.hd; e += blockDim.x) {
+      float t = 0.f;
+#pragma unroll
+      for (int k = 0; k < kQkWarps; ++k) t += sums[k][e];
+      p.part[(long long)blockIdx.x * p.hd + e] = t;
     }
+  }
+}
+
+// Adds the partial rows of the queries' (blockIdx.y = 0) and the keys' blocks,
+// in order: 32 columns and 16 runs of rows a block.
+__global__ void __launch_bounds__(512) qk_gain_kernel(const float *__restrict__ part, int nq, int nqk,
+                                                      int hd, float *__restrict__ dgq,
+                                                      float *__restrict__ dgk) {
+  __shared__ float sm[16][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int lo = blockIdx.y ? nq : 0, hi = blockIdx.y ? nqk : nq;
+  float s = 0.f;
+  if (c < hd) {
+#pragma unroll 4
+    for (int b = lo + threadIdx.y; b < hi; b += 16) s += part[(long long)b * hd + c];
+  }
+  sm[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * p.hd; c += blockDim.x) {
-    float s = 0.f;
+  if (threadIdx.y == 0 && c < hd) {
+    float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < kQkWarps; ++w) s += sums[w][c];
-    const int kind = c >= p.hd;
-    p.part[((long long)kind * gridDim.x + blockIdx.x) * p.hd + (c - kind * p.hd)] = s;
+    for (int i = 0; i < 16; ++i) t += sm[i][threadIdx.x];
+    (blockIdx.y ? dgk : dgq)[c] = t;
   }
 }
 
@@ -358,7 +367,7 @@ int check_qk(const gptl_qk_desc &d, gptl_dtype dt, gptl_qk_desc *out) {
     return GPTL_E_SHAPE;
   const long long heads = (long long)d.q_heads + d.k_heads + d.v_heads;
   const long long rows = (long long)d.tokens * d.groups;
-  if (heads > (1 << 20) || rows >= (1ll << 31)) return GPTL_E_SHAPE;
+  if (heads > (1 << 20) || rows >= (1ll << 30)) return GPTL_E_SHAPE;
   const long long width = heads * d.head_dim;
   if (d.interleaved != 0 && d.interleaved != 1) return GPTL_E_ARG;
   long long *str[2][2] = {{&out->x_ld, &out->x_gstride}, {&out->y_ld, &out->y_gstride}};
@@ -394,47 +403,94 @@ int qk_lanes(int hd) {                    // lanes per head: a power of two >= h
   return l;
 }
 
-// Fills the launch-independent fields and picks the split of a token's heads
-// over warps: whole tokens once they give every resident warp several, else
-// chunks of head slots, down to one slot a warp for a handful of tokens.  Value
-// heads do not enter the split, so in place or not, the sums have one order.
-QkParams qk_params(const gptl_qk_desc &d, int v_heads, int warps) {
+// Sizes, and the split of the work over `blocks` resident blocks.  Queries and
+// keys get blocks of their own, in proportion to their slots (a token's angles
+// cost `angles` of them), so that a warp keeps one gain and its gradient in
+// registers.  A token's slots go to one warp, or in chunks to several where
+// that evens out the tokens of a warp: the number of chunks is the one with
+// the shortest longest warp.  Value heads come in blocks behind the others:
+// with or without them, the sums have one order.
+QkParams qk_params(const gptl_qk_desc &d, int v_heads, int blocks, double angles) {
   QkParams p{};
   const int hpw = 32 / qk_lanes(d.head_dim);
-  p.slots_q = (d.q_heads + hpw - 1) / hpw;
-  p.slots_k = (d.k_heads + hpw - 1) / hpw;
-  p.slots_v = (v_heads + hpw - 1) / hpw;
-  const int slots = p.slots_q + p.slots_k;
-  const long long rows = (long long)d.tokens * d.groups;
-  long long chunks = (4ll * warps + rows - 1) / rows;
-  if (chunks > slots) chunks = slots;
-  p.spc = (unsigned)((slots + chunks - 1) / chunks);
-  p.chunks = (unsigned)((slots + p.spc - 1) / p.spc);
-  p.items = (unsigned)(rows * p.chunks);
+  const int heads[2] = {d.q_heads, d.k_heads};
+  if (d.rot_dim == 0) angles = 0.25;
+  double weight[2];
+  for (int i = 0; i < 2; ++i) {
+    QkKind &k = p.kind[i];
+    k.heads = heads[i];
+    k.first = i ? d.q_heads : 0;
+    k.slots = (heads[i] + hpw - 1) / hpw;
+    weight[i] = angles + (double)k.slots * d.groups;
+  }
+  for (int i = 0; i < 2; ++i) {
+    QkKind &k = p.kind[i];
+    const int all = k.slots * d.groups;
+    long long nb = (long long)(blocks * weight[i] / (weight[0] + weight[1]));
+    const long long most = ((long long)d.tokens * all + kQkWarps - 1) / kQkWarps;
+    if (nb > most) nb = most;
+    if (nb < 1) nb = 1;
+    const long long warps = nb * kQkWarps;
+    double best = 0;
+    k.chunks = 0;
+    for (int c = 1; c <= all && c <= warps && c <= 64; ++c) {
+      const int spc = (all + c - 1) / c;
+      if (c > 1 && spc == k.spc) continue;                 // the same chunks, some of them empty
+      const long long each = warps / c;
+      const double longest = (double)((d.tokens + each - 1) / each) * (angles + (double)spc);
+      if (!k.chunks || longest < best) {
+        best = longest;
+        k.spc = spc;
+        k.chunks = (all + spc - 1) / spc;
+      }
+    }
+    k.warps = (int)(warps / k.chunks);
+    if (i == 0) p.blocks_q = (int)nb;
+    else p.blocks_qk = p.blocks_q + (int)nb;
+  }
+  p.v_vecs = v_heads * d.head_dim / 8;
+  p.v_first = (d.q_heads + d.k_heads) * d.head_dim / 8;
+  if (v_heads) {
+    const long long rows = (long long)d.tokens * d.groups, want = 8ll * blocks;
+    const long long nb = (rows + kQkWarps - 1) / kQkWarps;
+    p.v_blocks = (int)(nb < want ? nb : want);
+  }
   p.x_ld = d.x_ld; p.x_gs = d.x_gstride; p.y_ld = d.y_ld; p.y_gs = d.y_gstride;
-  p.tokens = d.tokens; p.q = d.q_heads; p.k = d.k_heads; p.v = v_heads; p.hd = d.head_dim;
-  p.rot = d.rot_dim; p.axes = d.axes; p.seq = d.seq; p.interleaved = d.interleaved;
+  p.tokens = d.tokens; p.groups = d.groups; p.hd = d.head_dim;
+  p.rot = d.rot_dim; p.axes = d.axes; p.seq = d.seq;
   p.eps = d.eps; p.inv_hd = 1.0f / (float)d.head_dim;
   return p;
 }
 
 template <bool BWD>
-int qk_launch(const QkParams &p, gptl_dtype dt, unsigned grid, cudaStream_t st) {
-  auto go = [&]<typename T, int LPH>() {
-    if constexpr (BWD) qk_rope_bwd_kernel<T, LPH><<<grid, kQkWarps * 32, 0, st>>>(p);
-    else qk_rope_fwd_kernel<T, LPH><<<grid, kQkWarps * 32, 0, st>>>(p);
+int qk_launch(const QkParams &p, gptl_dtype dt, bool interleaved, cudaStream_t st) {
+  const unsigned grid = (unsigned)(p.blocks_qk + p.v_blocks);
+  const bool norm = p.gain[0] != nullptr;
+  int rc = GPTL_OK;
+  auto run = [&]<typename T, int LPH, bool INTER, bool NORM>() {
+    auto kern = qk_rope_kernel<T, LPH, INTER, NORM, BWD>;
+    kern<<<grid, kQkWarps * 32, 0, st>>>(p);
+  };
+  auto go = [&]<typename T, int LPH, bool INTER>() {
+    if (norm) run.template operator()<T, LPH, INTER, true>();
+    else run.template operator()<T, LPH, INTER, false>();
+  };
+  auto by_pairs = [&]<typename T, int LPH>() {
+    if (interleaved) go.template operator()<T, LPH, true>();
+    else go.template operator()<T, LPH, false>();
   };
   auto by_lanes = [&]<typename T>() {
     switch (qk_lanes(p.hd)) {
-      case 1: go.template operator()<T, 1>(); break;
-      case 2: go.template operator()<T, 2>(); break;
-      case 4: go.template operator()<T, 4>(); break;
-      case 8: go.template operator()<T, 8>(); break;
-      default: go.template operator()<T, 16>(); break;
+      case 1: by_pairs.template operator()<T, 1>(); break;
+      case 2: by_pairs.template operator()<T, 2>(); break;
+      case 4: by_pairs.template operator()<T, 4>(); break;
+      case 8: by_pairs.template operator()<T, 8>(); break;
+      default: by_pairs.template operator()<T, 16>(); break;
     }
   };
   if (dt == GPTL_FP16) by_lanes.template operator()<__half>();
   else by_lanes.template operator()<__nv_bfloat16>();
+  GPTL_TRY(rc);
   GPTL_CK(cudaGetLastError());
   prof_launched(st, BWD ? GPTL_KIND_QK_ROPE_BWD : GPTL_KIND_QK_ROPE_FWD);
   return GPTL_OK;
@@ -497,17 +553,15 @@ int gptl_qk_norm_rope_fwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   int sms = 0;
   GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  QkParams p = qk_params(d, in_place ? 0 : d.v_heads, sms * 3 * kQkWarps);
+  QkParams p = qk_params(d, in_place ? 0 : d.v_heads, sms * kQkFwdBlocks, kQkFwdAngles);
   p.x = x;
   p.out = y;
-  p.gq = gq;
-  p.gk = gk;
+  p.gain[0] = gq;
+  p.gain[1] = gk;
   p.pos = pos;
   p.table = table;
-  unsigned grid = (p.items + kQkWarps - 1) / kQkWarps;
-  if (grid > 3u * sms) grid = 3u * sms;
   prof_start(st);
-  return qk_launch<false>(p, dtype, grid, st);
+  return qk_launch<false>(p, dtype, d.interleaved, st);
 }
 
 size_t gptl_qk_norm_rope_scratch_bytes(const gptl_qk_desc *desc) {
@@ -535,23 +589,25 @@ int gptl_qk_norm_rope_bwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   int sms = 0;
   GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  unsigned most = 2u * sms;
+  int most = sms * kQkBwdBlocks;
   if (most > kQkMaxBlocks) most = kQkMaxBlocks;
-  QkParams p = qk_params(d, dy == dx ? 0 : d.v_heads, (int)most * kQkWarps);
+  QkParams p = qk_params(d, dy == dx ? 0 : d.v_heads, most, kQkBwdAngles);
   p.x = x;
   p.dy = dy;
   p.out = dx;
-  p.gq = gq;
-  p.gk = gk;
+  p.gain[0] = gq;
+  p.gain[1] = gk;
   p.pos = pos;
   p.table = table;
   p.part = static_cast<float *>(scratch);
-  unsigned grid = (p.items + kQkWarps - 1) / kQkWarps;
-  if (grid > most) grid = most;
   prof_start(st);
-  GPTL_TRY(qk_launch<true>(p, dtype, grid, st));
+  GPTL_TRY(qk_launch<true>(p, dtype, d.interleaved, st));
   if (!gq) return GPTL_OK;
-  return launch_reduce_parts(p.part, (int)grid, d.head_dim, 2, dgq, dgk, nullptr, nullptr, st);
+  qk_gain_kernel<<<dim3((d.head_dim + 31) / 32, 2), dim3(32, 16), 0, st>>>(
+      p.part, p.blocks_q, p.blocks_qk, d.head_dim, dgq, dgk);
+  GPTL_CK(cudaGetLastError());
+  prof_launched(st, GPTL_KIND_REDUCE);
+  return GPTL_OK;
 }
 
 }  // extern "C"
