@@ -38,6 +38,9 @@ CASES = [
     ("bf16", 19, 3, 7, 2, 2, 112, 0, 0, 1, 9),               # no rotation
     ("bf16", 700, 1, 9, 1, 1, 96, 48, 1, 1, "seq"),          # shared key head, many tokens
     ("fp16", 3000, 2, 2, 2, 2, 32, 32, 0, 2, 50),            # every resident warp has tokens
+    ("bf16", 41, 3, 5, 2, 0, 144, 96, 0, 1, 70),             # nine lanes a head
+    ("fp16", 90, 2, 4, 3, 1, 160, 160, 1, 2, 70),            # ten
+    ("bf16", 23, 1, 6, 2, 1, 176, 176, 0, 1, 5000),          # eleven of sixteen
 ]
 
 

@@ -26,14 +26,14 @@ namespace gptl {
 constexpr int kQkWarps = 8;             // warps of a block
 constexpr int kQkMaxBlocks = 592;       // partial rows of the gains' gradients
 constexpr int kQkFwdBlocks = 4, kQkBwdBlocks = 2;              // resident on an SM
-constexpr double kQkFwdAngles = 4.0, kQkBwdAngles = 2.0;       // a token's angles, in slots
+constexpr double kQkAngles = 1.0;       // cost of a token's angles, in slots
 
-// The heads of one kind.  A slot is a warp's step: 32/LPH neighbouring heads of
-// one group.  A chunk is `spc` slots of the groups * slots of a token.
+// The heads of one kind.  A slot is a warp's step: 32/lanes heads of a token, counted
+// through all groups.
 struct QkKind {
   int heads, first;                     // heads of a group, the first one's place in the row
-  int slots, chunks, spc;
-  int warps;                            // warps of one chunk: they share its tokens
+  int slots;                            // of a token
+  int warps;                            // they share the tokens' slots evenly
 };
 
 struct QkParams {
@@ -48,78 +48,127 @@ struct QkParams {
   int blocks_q, blocks_qk;              // blocks [0, blocks_q), [blocks_q, blocks_qk), then values
   int v_vecs, v_first, v_blocks;        // 16-byte vectors of a row's values, the first's place
   int tokens, groups, hd, rot, axes, seq;
+  int lanes, heads_per_warp;            // lanes of a head (see qk_lanes)
   float eps, inv_hd;
 };
+
+// The rotated pairs' turns, as 64-bit fractions of a turn, and axes, in shared
+// memory.  Position times fraction, modulo 2^64, is the fraction of a turn that is
+// left, with no rounding: far positions keep all their bits, and the loop over
+// tokens needs no fp64.
+struct QkTurns {
+  unsigned long long turn[128];
+  int axis[128];
+};
+
+__device__ __forceinline__ void qk_load_turns(const QkParams &p, QkTurns &t) {
+  for (int j = threadIdx.x; j < p.rot / 2; j += blockDim.x) {
+    const gptl_rope_pair e = p.table[j];
+    t.turn[j] = __double2ull_rn((e.turns - floor(e.turns)) * 18446744073709551616.0);
+    t.axis[j] = e.axis;
+    if ((unsigned)e.axis >= (unsigned)p.axes) {
+      set_device_error(kErrIndex);
+      t.axis[j] = 0;
+    }
+  }
+}
 
 // Sines and cosines of one token's pairs, by the whole warp.  Lane c of a head
 // holds pairs 8c .. 8c + 7; cs[i * lanes + c] = cosines of its pairs 2i and 2i + 1,
 // then their sines, so that the lanes of a head read 16 neighbouring bytes each.
-__device__ __forceinline__ void qk_angles(const QkParams &p, int token, float4 *cs, int lanes, int lane) {
+// sin.approx and cos.approx are good to 2^-20 in [-pi, pi], a hundredth of a
+// rounding step of the outputs and less.
+__device__ __forceinline__ void qk_angles(const QkParams &p, const QkTurns &t, int token, float4 *cs,
+                                          int lane) {
   __syncwarp();
-  for (int j = lane; j < p.rot / 2; j += 32) {
-    const gptl_rope_pair e = p.table[j];
-    int axis = e.axis;
-    if ((unsigned)axis >= (unsigned)p.axes) {
-      set_device_error(kErrIndex);
-      axis = 0;
-    }
-    const int at = p.pos ? __ldg(p.pos + (long long)axis * p.tokens + token) : token % p.seq;
-    double t = (double)at * e.turns;
-    t -= rint(t);
-    float s, c;
-    sincospif(2.0f * (float)t, &s, &c);
-    float *to = reinterpret_cast<float *>(cs + (j % 8 / 2) * lanes + j / 8) + j % 2;
-    to[0] = c;
-    to[2] = s;
+  float *to = reinterpret_cast<float *>(cs + (lane % 8 / 2) * p.lanes + lane / 8) + lane % 2;
+  const int by_row = p.pos ? 0 : token % p.seq;
+  for (int j = lane; j < p.rot / 2; j += 32, to += 16) {
+    const int at = p.pos ? __ldg(p.pos + (long long)t.axis[j] * p.tokens + token) : by_row;
+    const long long left = (long long)((unsigned long long)(long long)at * t.turn[j]);
+    const float phi = (float)(int)(left >> 32) * 1.4629180792671596e-9f;      // 2 pi / 2^32
+    to[0] = __cosf(phi);
+    to[2] = __sinf(phi);
   }
   __syncwarp();
 }
 
-// A lane's 8 pairs (a, b): v0 and v1 hold them as neighbours (INTER) or as the
-// vectors of first and of second elements.
+// A lane's 8 pairs (a, b), two to a register pair: v0 and v1 hold them as
+// neighbours (INTER) or as the vectors of first and of second elements.
 template <typename T, bool INTER>
-__device__ __forceinline__ void qk_unpack(const uint4 &v0, const uint4 &v1, float (&a)[8],
-                                          float (&b)[8]) {
-  if constexpr (INTER) {
-    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+__device__ __forceinline__ void qk_unpack(const uint4 &v0, const uint4 &v1, float2 (&a)[4],
+                                          float2 (&b)[4]) {
+  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 q = Cvt<T>::unpack2(w[i]);
-      a[i] = q.x;
-      b[i] = q.y;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (INTER) {
+      const float2 p = Cvt<T>::unpack2(w[2 * i]), q = Cvt<T>::unpack2(w[2 * i + 1]);
+      a[i] = make_float2(p.x, q.x);
+      b[i] = make_float2(p.y, q.y);
+    } else {
+      a[i] = Cvt<T>::unpack2(w[i]);
+      b[i] = Cvt<T>::unpack2(w[4 + i]);
     }
-  } else {
-    unpack8<T>(v0, a);
-    unpack8<T>(v1, b);
   }
 }
 template <typename T, bool INTER>
-__device__ __forceinline__ void qk_pack(const float (&a)[8], const float (&b)[8], uint4 &v0, uint4 &v1) {
-  if constexpr (INTER) {
-    uint32_t w[8];
+__device__ __forceinline__ void qk_pack(const float2 (&a)[4], const float2 (&b)[4], uint4 &v0,
+                                        uint4 &v1) {
+  uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = Cvt<T>::pack2(a[i], b[i]);
-    v0 = make_uint4(w[0], w[1], w[2], w[3]);
-    v1 = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
-    v0 = pack8<T>(a);
-    v1 = pack8<T>(b);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (INTER) {
+      w[2 * i] = Cvt<T>::pack2(a[i].x, b[i].x);
+      w[2 * i + 1] = Cvt<T>::pack2(a[i].y, b[i].y);
+    } else {
+      w[i] = Cvt<T>::pack2(a[i].x, a[i].y);
+      w[4 + i] = Cvt<T>::pack2(b[i].x, b[i].y);
+    }
   }
+  v0 = make_uint4(w[0], w[1], w[2], w[3]);
+  v1 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// Turns the pairs (a, b) by (cos, dir * sin) of the lane's table entries.
-__device__ __forceinline__ void qk_turn(float (&a)[8], float (&b)[8], const float4 *cs, int lanes,
-                                        float dir) {
+// Turns the pairs (a, b) by the lane's table entries, or (BACK) the other way.
+template <bool BACK>
+__device__ __forceinline__ void qk_turn(float2 (&a)[4], float2 (&b)[4], const float4 *cs, int lanes) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 q = cs[i * lanes];
-    const float c[2] = {q.x, q.y}, s[2] = {dir * q.z, dir * q.w};
+    const float2 c = make_float2(q.x, q.y), s = make_float2(q.z, q.w), n = make_float2(-q.z, -q.w);
+    const float2 x = a[i];
+    a[i] = fma2(x, c, mul2(b[i], BACK ? s : n));
+    b[i] = fma2(b[i], c, mul2(x, BACK ? n : s));
+  }
+}
+
+// Sums of v and w over a head's lanes, the same bits in each.  LANES = 0: a power
+// of two of lanes (p.lanes), in a butterfly; else that number, added in lane order,
+// in two steps where it has two factors.
+template <int LANES, bool TWO>
+__device__ __forceinline__ void qk_head_sum(const QkParams &p, int lane, int c, float &v, float &w) {
+  if constexpr (LANES == 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = a[2 * i + e], y = b[2 * i + e];
-      a[2 * i + e] = fmaf(x, c[e], -(y * s[e]));
-      b[2 * i + e] = fmaf(y, c[e], x * s[e]);
-    }
+    for (int o = 8; o > 0; o >>= 1)
+      if (o < p.lanes) {
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        if constexpr (TWO) w += __shfl_xor_sync(0xffffffffu, w, o);
+      }
+  } else {
+    constexpr int R0 = LANES == 9 ? 3 : LANES % 2 == 0 ? 2 : LANES, R1 = LANES / R0;
+    auto add = [&](int from, int n, int stride) {
+      float a = __shfl_sync(0xffffffffu, v, from), b = 0.f;
+      if constexpr (TWO) b = __shfl_sync(0xffffffffu, w, from);
+#pragma unroll
+      for (int k = 1; k < n; ++k) {
+        a += __shfl_sync(0xffffffffu, v, from + k * stride);
+        if constexpr (TWO) b += __shfl_sync(0xffffffffu, w, from + k * stride);
+      }
+      v = a;
+      w = b;
+    };
+    add(lane - c % R0, R0, 1);
+    if constexpr (R1 > 1) add(lane - c + c % R0, R1, R0);
   }
 }
 
@@ -143,14 +192,15 @@ __device__ void qk_copy_values(const QkParams &p, const T *from, long long f_ld,
 }
 
 // BWD: out = dx from x and dy; else out = y from x.  NORM: with gains.
-template <typename T, int LPH, bool INTER, bool NORM, bool BWD>
+template <typename T, int LANES, bool INTER, bool NORM, bool BWD>
 __global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBlocks)
     qk_rope_kernel(const QkParams p) {
-  constexpr int HPW = 32 / LPH;
   constexpr bool kX = NORM || !BWD;                        // x is read
-  __shared__ __align__(16) float4 cs_all[kQkWarps][4 * LPH];
-  __shared__ __align__(16) float4 gain_all[NORM ? 4 * LPH : 1];   // as cs_all: (a, a, b, b)
+  __shared__ __align__(16) float4 cs_all[kQkWarps][4 * 16];
+  __shared__ __align__(16) float4 gain_all[NORM ? 4 * 16 : 1];   // as cs_all: (a, a, b, b)
+  __shared__ QkTurns turns_all;
   __shared__ float sums[BWD && NORM ? kQkWarps : 1][256];
+  if constexpr (BWD && NORM) grid_dependents_launch();
   const T *in_x = static_cast<const T *>(p.x), *in_dy = static_cast<const T *>(p.dy);
   T *out = static_cast<T *>(p.out);
   if ((int)blockIdx.x >= p.blocks_qk) {
@@ -164,45 +214,56 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBloc
   const int w = ((int)blockIdx.x - (key ? p.blocks_q : 0)) * kQkWarps + warp;
 
   // the lane's 16 elements of a head: two vectors of 8 at v0 and v1
-  const int c = lane % LPH, sub = lane / LPH;
-  const bool on = c < p.hd / 16, turns = c < p.rot / 16;
+  const int LPH = LANES ? LANES : p.lanes, HPW = LANES ? 32 / LANES : p.heads_per_warp;
+  const int sub = lane / LPH, c = lane - sub * LPH;
+  const bool on = c < p.hd / 16 && sub < HPW, turns = on && c < p.rot / 16;
   const bool split = turns && !INTER;                      // partners rot/2 apart
   const int v0 = !on ? 0 : split ? 8 * c : 16 * c, v1 = split ? v0 + p.rot / 2 : v0 + 8;
 
+  qk_load_turns(p, turns_all);
   if constexpr (NORM) {
     if (warp == 0 && lane < LPH) {
       const T *g = static_cast<const T *>(p.gain[key]);
-      float ga[8] = {}, gb[8] = {};                        // 0 beyond the head's elements
+      float2 ga[4] = {}, gb[4] = {};                       // 0 beyond the head's elements
       if (on)
         qk_unpack<T, INTER>(*reinterpret_cast<const uint4 *>(g + v0),
                             *reinterpret_cast<const uint4 *>(g + v1), ga, gb);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        gain_all[i * LPH + c] = make_float4(ga[2 * i], ga[2 * i + 1], gb[2 * i], gb[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) gain_all[i * LPH + c] = make_float4(ga[i].x, ga[i].y, gb[i].x, gb[i].y);
     }
-    __syncthreads();
   }
+  __syncthreads();
   const float4 *gain = gain_all + c, *cs = cs_all[warp] + c;
-  float acc_a[8] = {}, acc_b[8] = {};                      // the gain's gradient
+  float2 acc_a[4] = {}, acc_b[4] = {};                     // the gain's gradient
 
-  const int chunk = w / K.warps;
-  const int u0 = chunk * K.spc, n_slots = min(K.spc, p.groups * K.slots - u0);
-  const int g0 = u0 / K.slots, s0 = u0 - g0 * K.slots;
-  const int step = HPW * p.hd, dv = v1 - v0;
-  const long long col = (long long)s0 * step + (K.first + sub) * p.hd + v0;
-  const long long x_wrap = p.x_gs - (long long)K.slots * step, y_wrap = p.y_gs - (long long)K.slots * step;
-  const int h_last = on ? K.heads - sub : 0;               // a head in slot s where s * HPW < h_last
-  for (int token = chunk < K.chunks ? w - chunk * K.warps : p.tokens; token < p.tokens;
-       token += K.warps) {
-    // the next slot to fetch: its number within the group, its places
-    int hs = s0 * HPW;
+  // the warp's share of all tokens' slots, and its steps from slot to slot
+  const int all = p.groups * K.heads;
+  const int dg = HPW / K.heads, dh = HPW - dg * K.heads, dv = v1 - v0;
+  const int g_sub = sub / K.heads, h_sub = sub - g_sub * K.heads;
+  const long long x_step = dg * p.x_gs + dh * p.hd, x_wrap = p.x_gs - (long long)K.heads * p.hd;
+  const long long y_step = dg * p.y_gs + dh * p.hd, y_wrap = p.y_gs - (long long)K.heads * p.hd;
+  const long long total = (long long)p.tokens * K.slots;
+  const long long lo = total * w / K.warps;
+  int left = (int)(total * (w + 1) / K.warps - lo);
+  int token = (int)(lo / K.slots), s0 = (int)(lo - (long long)token * K.slots);
+  for (int n_slots; left > 0; left -= n_slots, ++token, s0 = 0) {
+    n_slots = min(K.slots - s0, left);
+    const int first = s0 * HPW + sub;                      // the lane's head among all
+    int g0 = g_sub, h0 = h_sub;
+    if (s0) {
+      g0 = first / K.heads;
+      h0 = first - g0 * K.heads;
+    }
+    const int col = (K.first + h0) * p.hd + v0;
+    // the next slot to fetch: the lane's head, its number in all, its places
+    int h = h0, n = first;
     const T *px = in_x + g0 * p.x_gs + token * p.x_ld + col;
     const T *pd = in_dy + g0 * p.y_gs + token * p.y_ld + col;
     T *po = out + g0 * p.y_gs + token * p.y_ld + col, *o = po;
     uint4 nx0, nx1, nd0, nd1;
     bool live, here;
     auto fetch = [&]() {
-      live = hs < h_last;
+      live = on && n < all;
       o = po;
       if (live) {
         if constexpr (kX) {
@@ -216,83 +277,77 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBloc
       } else {
         nx0 = nx1 = nd0 = nd1 = uint4{};
       }
-      hs += HPW;
-      px += step;
-      pd += step;
-      po += step;
-      if (hs >= K.heads) {
-        hs = 0;
+      n += HPW;
+      h += dh;
+      px += x_step;
+      pd += y_step;
+      po += y_step;
+      if (h >= K.heads) {
+        h -= K.heads;
         px += x_wrap;
         pd += y_wrap;
         po += y_wrap;
       }
     };
     fetch();
-    if (p.rot) qk_angles(p, token, cs_all[warp], LPH, lane);
+    if (p.rot) qk_angles(p, turns_all, token, cs_all[warp], lane);
     for (int u = 0; u < n_slots; ++u) {
       {
         const uint4 x0 = nx0, x1 = nx1, d0 = nd0, d1 = nd1;
         T *to = o;
         here = live;
         if (u + 1 < n_slots) fetch();                      // the next slot's loads go out first
-        float a[8], b[8];
+        float2 a[4], b[4];
         if constexpr (BWD) {
           qk_unpack<T, INTER>(d0, d1, a, b);
-          if (turns) qk_turn(a, b, cs, LPH, -1.f);
+          if (turns) qk_turn<true>(a, b, cs, LPH);
         }
         if constexpr (NORM) {
-          float xa[8], xb[8], ss = 0.f, sd = 0.f;
+          float2 xa[4], xb[4], s2 = make_float2(0.f, 0.f), d2 = s2;
           qk_unpack<T, INTER>(x0, x1, xa, xb);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+          for (int i = 0; i < 4; ++i) s2 = fma2(xa[i], xa[i], fma2(xb[i], xb[i], s2));
+          float ss = s2.x + s2.y, sd = 0.f;
           if constexpr (BWD) {
             // the gain's gradient takes dn x, then dn becomes d = dn g
-            float ta[8], tb[8];
+            float2 ta[4], tb[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 g = gain[i * LPH];
-              const float ga[2] = {g.x, g.y}, gb[2] = {g.z, g.w};
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int k = 2 * i + e;
-                ta[k] = a[k] * xa[k];
-                tb[k] = b[k] * xb[k];
-                sd = fmaf(ta[k], ga[e], fmaf(tb[k], gb[e], sd));
-                a[k] *= ga[e];
-                b[k] *= gb[e];
-              }
+              const float2 ga = make_float2(g.x, g.y), gb = make_float2(g.z, g.w);
+              ta[i] = mul2(a[i], xa[i]);
+              tb[i] = mul2(b[i], xb[i]);
+              d2 = fma2(ta[i], ga, fma2(tb[i], gb, d2));
+              a[i] = mul2(a[i], ga);
+              b[i] = mul2(b[i], gb);
             }
-#pragma unroll
-            for (int o2 = LPH / 2; o2 > 0; o2 >>= 1) {
-              ss += __shfl_xor_sync(0xffffffffu, ss, o2);
-              sd += __shfl_xor_sync(0xffffffffu, sd, o2);
-            }
+            sd = d2.x + d2.y;
+            qk_head_sum<LANES, true>(p, lane, c, ss, sd);
             const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
             const float m = -r * r * r * (sd * p.inv_hd);
+            const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              acc_a[k] = fmaf(ta[k], r, acc_a[k]);
-              acc_b[k] = fmaf(tb[k], r, acc_b[k]);
-              a[k] = fmaf(a[k], r, xa[k] * m);
-              b[k] = fmaf(b[k], r, xb[k] * m);
+            for (int i = 0; i < 4; ++i) {
+              acc_a[i] = fma2(ta[i], r2, acc_a[i]);
+              acc_b[i] = fma2(tb[i], r2, acc_b[i]);
+              a[i] = fma2(a[i], r2, mul2(xa[i], m2));
+              b[i] = fma2(b[i], r2, mul2(xb[i], m2));
             }
           } else {
-#pragma unroll
-            for (int o2 = LPH / 2; o2 > 0; o2 >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o2);
+            qk_head_sum<LANES, false>(p, lane, c, ss, sd);
             const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+            const float2 r2 = make_float2(r, r);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 g = gain[i * LPH];
-              a[2 * i] = xa[2 * i] * r * g.x;
-              a[2 * i + 1] = xa[2 * i + 1] * r * g.y;
-              b[2 * i] = xb[2 * i] * r * g.z;
-              b[2 * i + 1] = xb[2 * i + 1] * r * g.w;
+              a[i] = mul2(mul2(xa[i], r2), make_float2(g.x, g.y));
+              b[i] = mul2(mul2(xb[i], r2), make_float2(g.z, g.w));
             }
           }
         } else if constexpr (!BWD) {
           qk_unpack<T, INTER>(x0, x1, a, b);
         }
-        if (!BWD && turns) qk_turn(a, b, cs, LPH, 1.f);
+        if (!BWD && turns) qk_turn<false>(a, b, cs, LPH);
         if (here) {
           uint4 q0, q1;
           qk_pack<T, INTER>(a, b, q0, q1);
@@ -306,20 +361,26 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBloc
     // the warp's head positions, then the block's warps, each in a fixed order
     float f[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {                          // in the order of v0 and v1
-      f[INTER ? 2 * i : i] = acc_a[i];
-      f[INTER ? 2 * i + 1 : 8 + i] = acc_b[i];
+    for (int i = 0; i < 4; ++i) {                          // in the order of v0 and v1
+      f[INTER ? 4 * i : 2 * i] = acc_a[i].x;
+      f[INTER ? 4 * i + 2 : 2 * i + 1] = acc_a[i].y;
+      f[INTER ? 4 * i + 1 : 8 + 2 * i] = acc_b[i].x;
+      f[INTER ? 4 * i + 3 : 9 + 2 * i] = acc_b[i].y;
     }
+    if constexpr (LANES == 0) {
+      for (int o = LPH; o < 32; o <<= 1)
 #pragma unroll
-    for (int o = LPH; o < 32; o <<= 1)
+        for (int i = 0; i < 16; ++i) f[i] += __shfl_xor_sync(0xffffffffu, f[i], o);
+    }
+    for (int k = 0; k < (LANES == 0 ? 1 : HPW); ++k) {
+      if (sub == k && on)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] += __shfl_xor_sync(0xffffffffu, f[i], o);
-    if (lane < LPH && on)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[warp][v0 + i] = f[i];
-        sums[warp][v1 + i] = f[8 + i];
-      }
+        for (int i = 0; i < 8; ++i) {
+          sums[warp][v0 + i] = f[i] + (k ? sums[warp][v0 + i] : 0.f);
+          sums[warp][v1 + i] = f[8 + i] + (k ? sums[warp][v1 + i] : 0.f);
+        }
+      __syncwarp();
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < p.hd; e += blockDim.x) {
       float t = 0.f;
@@ -339,6 +400,7 @@ __global__ void __launch_bounds__(512) qk_gain_kernel(const float *__restrict__ 
   const int c = blockIdx.x * 32 + threadIdx.x;
   const int lo = blockIdx.y ? nq : 0, hi = blockIdx.y ? nqk : nq;
   float s = 0.f;
+  grid_dependency_wait();
   if (c < hd) {
 #pragma unroll 4
     for (int b = lo + threadIdx.y; b < hi; b += 16) s += part[(long long)b * hd + c];
@@ -357,6 +419,23 @@ __global__ void __launch_bounds__(512) qk_gain_kernel(const float *__restrict__ 
 
 namespace {
 
+// Launches a kernel that may be brought up while the one before it on the stream
+// still runs; the kernel itself waits for that one's results.
+template <typename... P, typename... A>
+int launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  GPTL_CK(cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...));
+  return GPTL_OK;
+}
+
 // Sizes and strides of a descriptor; dense strides filled in.
 int check_qk(const gptl_qk_desc &d, gptl_dtype dt, gptl_qk_desc *out) {
   if (dt != GPTL_FP16 && dt != GPTL_BF16) return GPTL_E_DTYPE;
@@ -367,7 +446,7 @@ int check_qk(const gptl_qk_desc &d, gptl_dtype dt, gptl_qk_desc *out) {
     return GPTL_E_SHAPE;
   const long long heads = (long long)d.q_heads + d.k_heads + d.v_heads;
   const long long rows = (long long)d.tokens * d.groups;
-  if (heads > (1 << 20) || rows >= (1ll << 30)) return GPTL_E_SHAPE;
+  if (heads * d.groups > (1 << 20) || rows >= (1ll << 30)) return GPTL_E_SHAPE;
   const long long width = heads * d.head_dim;
   if (d.interleaved != 0 && d.interleaved != 1) return GPTL_E_ARG;
   long long *str[2][2] = {{&out->x_ld, &out->x_gstride}, {&out->y_ld, &out->y_gstride}};
@@ -397,54 +476,46 @@ bool ranges_overlap(const void *a, long long na, const void *b, long long nb) {
   return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
 }
 
-int qk_lanes(int hd) {                    // lanes per head: a power of two >= head_dim / 16
+// Lanes of a head: one for each 16 elements where that lets a warp hold more heads
+// than the next power of two does (3, 5, 6, 9 and 10), else that power of two.
+int qk_lanes(int hd) {
+  const int n = hd / 16;
   int l = 1;
-  while (l < hd / 16) l *= 2;
-  return l;
+  while (l < n) l *= 2;
+  return 32 / n > 32 / l ? n : l;
 }
 
 // Sizes, and the split of the work over `blocks` resident blocks.  Queries and
 // keys get blocks of their own, in proportion to their slots (a token's angles
-// cost `angles` of them), so that a warp keeps one gain and its gradient in
-// registers.  A token's slots go to one warp, or in chunks to several where
-// that evens out the tokens of a warp: the number of chunks is the one with
-// the shortest longest warp.  Value heads come in blocks behind the others:
-// with or without them, the sums have one order.
-QkParams qk_params(const gptl_qk_desc &d, int v_heads, int blocks, double angles) {
+// cost about kQkAngles of them), so that a warp keeps one gain's gradient in
+// registers; the warps of a kind take equal runs of its tokens' slots, to the
+// slot, so that the last wave is as full as the others.  Value heads come in
+// blocks behind these: with or without them, the sums have one order.
+QkParams qk_params(const gptl_qk_desc &d, int v_heads, int blocks) {
   QkParams p{};
-  const int hpw = 32 / qk_lanes(d.head_dim);
+  const int lanes = qk_lanes(d.head_dim), hpw = 32 / lanes;
+  p.lanes = lanes;
+  p.heads_per_warp = hpw;
   const int heads[2] = {d.q_heads, d.k_heads};
-  if (d.rot_dim == 0) angles = 0.25;
+  const double angles = d.rot_dim ? kQkAngles : 0.0;
   double weight[2];
   for (int i = 0; i < 2; ++i) {
     QkKind &k = p.kind[i];
     k.heads = heads[i];
     k.first = i ? d.q_heads : 0;
-    k.slots = (heads[i] + hpw - 1) / hpw;
-    weight[i] = angles + (double)k.slots * d.groups;
+    k.slots = (int)(((long long)heads[i] * d.groups + hpw - 1) / hpw);
+    weight[i] = angles + (double)k.slots;
   }
   for (int i = 0; i < 2; ++i) {
     QkKind &k = p.kind[i];
-    const int all = k.slots * d.groups;
-    long long nb = (long long)(blocks * weight[i] / (weight[0] + weight[1]));
-    const long long most = ((long long)d.tokens * all + kQkWarps - 1) / kQkWarps;
+    long long nb = (long long)(blocks * weight[i] / (weight[0] + weight[1]) + 0.5);
+    const int free_blocks = i ? blocks - p.blocks_q : blocks - 1;   // one at least for the keys
+    if (nb > free_blocks) nb = free_blocks;
+    const long long total = (long long)d.tokens * k.slots;
+    const long long most = (total + kQkWarps - 1) / kQkWarps;
     if (nb > most) nb = most;
     if (nb < 1) nb = 1;
-    const long long warps = nb * kQkWarps;
-    double best = 0;
-    k.chunks = 0;
-    for (int c = 1; c <= all && c <= warps && c <= 64; ++c) {
-      const int spc = (all + c - 1) / c;
-      if (c > 1 && spc == k.spc) continue;                 // the same chunks, some of them empty
-      const long long each = warps / c;
-      const double longest = (double)((d.tokens + each - 1) / each) * (angles + (double)spc);
-      if (!k.chunks || longest < best) {
-        best = longest;
-        k.spc = spc;
-        k.chunks = (all + spc - 1) / spc;
-      }
-    }
-    k.warps = (int)(warps / k.chunks);
+    k.warps = (int)(nb * kQkWarps);
     if (i == 0) p.blocks_q = (int)nb;
     else p.blocks_qk = p.blocks_q + (int)nb;
   }
@@ -466,31 +537,26 @@ template <bool BWD>
 int qk_launch(const QkParams &p, gptl_dtype dt, bool interleaved, cudaStream_t st) {
   const unsigned grid = (unsigned)(p.blocks_qk + p.v_blocks);
   const bool norm = p.gain[0] != nullptr;
-  int rc = GPTL_OK;
-  auto run = [&]<typename T, int LPH, bool INTER, bool NORM>() {
-    auto kern = qk_rope_kernel<T, LPH, INTER, NORM, BWD>;
-    kern<<<grid, kQkWarps * 32, 0, st>>>(p);
+  auto run = [&]<typename T, int LANES, bool INTER, bool NORM>() {
+    qk_rope_kernel<T, LANES, INTER, NORM, BWD><<<grid, kQkWarps * 32, 0, st>>>(p);
   };
-  auto go = [&]<typename T, int LPH, bool INTER>() {
-    if (norm) run.template operator()<T, LPH, INTER, true>();
-    else run.template operator()<T, LPH, INTER, false>();
-  };
-  auto by_pairs = [&]<typename T, int LPH>() {
-    if (interleaved) go.template operator()<T, LPH, true>();
-    else go.template operator()<T, LPH, false>();
-  };
-  auto by_lanes = [&]<typename T>() {
-    switch (qk_lanes(p.hd)) {
-      case 1: by_pairs.template operator()<T, 1>(); break;
-      case 2: by_pairs.template operator()<T, 2>(); break;
-      case 4: by_pairs.template operator()<T, 4>(); break;
-      case 8: by_pairs.template operator()<T, 8>(); break;
-      default: by_pairs.template operator()<T, 16>(); break;
+  auto go = [&]<typename T, bool INTER>() {
+    if (!norm) return run.template operator()<T, 0, INTER, false>();      // no sums over lanes
+    switch (p.lanes) {
+      case 3: return run.template operator()<T, 3, INTER, true>();
+      case 5: return run.template operator()<T, 5, INTER, true>();
+      case 6: return run.template operator()<T, 6, INTER, true>();
+      case 9: return run.template operator()<T, 9, INTER, true>();
+      case 10: return run.template operator()<T, 10, INTER, true>();
+      default: return run.template operator()<T, 0, INTER, true>();
     }
   };
-  if (dt == GPTL_FP16) by_lanes.template operator()<__half>();
-  else by_lanes.template operator()<__nv_bfloat16>();
-  GPTL_TRY(rc);
+  auto by_pairs = [&]<typename T>() {
+    if (interleaved) go.template operator()<T, true>();
+    else go.template operator()<T, false>();
+  };
+  if (dt == GPTL_FP16) by_pairs.template operator()<__half>();
+  else by_pairs.template operator()<__nv_bfloat16>();
   GPTL_CK(cudaGetLastError());
   prof_launched(st, BWD ? GPTL_KIND_QK_ROPE_BWD : GPTL_KIND_QK_ROPE_FWD);
   return GPTL_OK;
@@ -553,7 +619,7 @@ int gptl_qk_norm_rope_fwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   int sms = 0;
   GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  QkParams p = qk_params(d, in_place ? 0 : d.v_heads, sms * kQkFwdBlocks, kQkFwdAngles);
+  QkParams p = qk_params(d, in_place ? 0 : d.v_heads, sms * kQkFwdBlocks);
   p.x = x;
   p.out = y;
   p.gain[0] = gq;
@@ -591,7 +657,7 @@ int gptl_qk_norm_rope_bwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int most = sms * kQkBwdBlocks;
   if (most > kQkMaxBlocks) most = kQkMaxBlocks;
-  QkParams p = qk_params(d, dy == dx ? 0 : d.v_heads, most, kQkBwdAngles);
+  QkParams p = qk_params(d, dy == dx ? 0 : d.v_heads, most);
   p.x = x;
   p.dy = dy;
   p.out = dx;
@@ -603,9 +669,8 @@ int gptl_qk_norm_rope_bwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   prof_start(st);
   GPTL_TRY(qk_launch<true>(p, dtype, d.interleaved, st));
   if (!gq) return GPTL_OK;
-  qk_gain_kernel<<<dim3((d.head_dim + 31) / 32, 2), dim3(32, 16), 0, st>>>(
-      p.part, p.blocks_q, p.blocks_qk, d.head_dim, dgq, dgk);
-  GPTL_CK(cudaGetLastError());
+  GPTL_TRY(launch_after(qk_gain_kernel, dim3((d.head_dim + 31) / 32, 2), dim3(32, 16), st,
+                        (const float *)p.part, p.blocks_q, p.blocks_qk, d.head_dim, dgq, dgk));
   prof_launched(st, GPTL_KIND_REDUCE);
   return GPTL_OK;
 }
