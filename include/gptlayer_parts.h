@@ -345,8 +345,8 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
  * stats, and entropy when dentropy is given, are the forward's.  dlogp needs
  * target; a row whose target is negative (or >= vocab, which also sets bit 2
  * of the device error word) takes dlogp = 0.  A row whose two gradients are
- * both 0 gets exact zeros without reading its logits; a row of -inf alone gets
- * zeros; a row with +inf or NaN gets NaN.  Columns from vocab to ld are not
+ * both 0 gets exact zeros whatever its logits; a row of -inf alone gets zeros; a
+ * row with +inf or NaN gets NaN.  Columns from vocab to ld are not
  * touched. */
 int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, int logits_f32,
                            const void *logits, const int *target, const float *stats,

@@ -18,17 +18,20 @@
 // a row; with few rows a cluster of up to 8 blocks shares it and joins its
 // parts through distributed shared memory, in one launch without scratch.
 //
-// Top alternatives: a thread remembers where it saw its maximum.  The k-th
-// largest of the threads' maxima (as 64-bit keys: value, then lowest index)
+// Top alternatives: a thread remembers in which vector it saw its maximum.  The
+// k-th largest of 64 groups' maxima (as 64-bit keys: value, then lowest index)
 // bounds the k-th largest element from below, so only threads whose maximum
-// reaches it hold candidates; a warp reads those threads' elements again (from
-// L2) and keeps its best 32 sorted in its lanes.  No list can overflow, and ties
-// fall to the lowest index by the key's order.
+// reaches it hold candidates, a few more than k of them as a rule; their
+// elements are read again (from L2), and a candidate's place is the number of
+// candidates above it.  Keys are distinct: ties fall to the lowest index, and
+// the order in which candidates are found does not matter.
 //
 // Included by libgptlayer.cu after gptlayer.cu, in the same translation unit.
 #pragma once
 
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "gptlayer_parts.h"
 
@@ -38,6 +41,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kLpMaxWarps = 16;
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpFill = 1, kLpNarrow = 8;
 constexpr int kLpBatch = 4;             // 16-byte loads of a thread in flight
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
@@ -47,11 +51,12 @@ struct LpParams {
   float *logp, *entropy, *stats, *top_logp;
   int *top_id;
   long long ld;
-  int rows, vocab, top_k, cluster;
+  int rows, vocab, top_k;
+  int cluster_log2;                     // blocks of a row
   // backward
   const float *in_stats, *in_entropy, *dlogp, *dentropy;
   void *dlogits;
-  int parts;                            // blocks of a row
+  int per;                              // vectors of a block
 };
 
 // ------------------------------------------------------- 16-byte vectors
@@ -140,6 +145,19 @@ __device__ __forceinline__ void lp_term(float x, float mr, float &z, float &s) {
   if constexpr (ENT) s = fmaf(e, fmaxf(t, -200.f), s);       // 2^t is 0 there; 0 * -inf is not
 }
 
+// The same for two elements at once.
+template <bool ENT>
+__device__ __forceinline__ void lp_terms(float2 x, float mr, float2 &z, float2 &s) {
+  float2 t = mul2(add2(x, make_float2(-mr, -mr)), make_float2(kLog2e, kLog2e));
+  const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+  z = add2(z, e);
+  if constexpr (ENT) {
+    t.x = fmaxf(t.x, -200.f);
+    t.y = fmaxf(t.y, -200.f);
+    s = fma2(e, t, s);
+  }
+}
+
 // ----------------------------------------------------------- sort keys
 // Order of (value, lowest index) as one 64-bit number; 0 is below all.
 __device__ __forceinline__ unsigned long long lp_key(float x, int index) {
@@ -153,86 +171,64 @@ __device__ __forceinline__ float lp_key_value(unsigned long long k) {
 }
 __device__ __forceinline__ int lp_key_index(unsigned long long k) { return (int)~(uint32_t)k; }
 
-__device__ __forceinline__ unsigned long long key_step(unsigned long long k, int lane, int o, bool up) {
-  const unsigned long long other = __shfl_xor_sync(0xffffffffu, k, o);
-  const bool keep_max = ((lane & o) == 0) != up;
-  return keep_max == (k > other) ? k : other;
-}
-// Sorts one key a lane, falling.
-__device__ __forceinline__ unsigned long long warp_sort(unsigned long long k, int lane) {
-#pragma unroll
-  for (int n = 2; n <= 32; n *= 2)
-#pragma unroll
-    for (int o = n / 2; o > 0; o /= 2) k = key_step(k, lane, o, (lane & n) != 0 && n < 32);
-  return k;
-}
-// The 32 largest of two falling lists, falling; `b` comes reversed.
-__device__ __forceinline__ unsigned long long warp_merge(unsigned long long a,
-                                                         unsigned long long b_reversed, int lane) {
-  unsigned long long k = a > b_reversed ? a : b_reversed;
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) k = key_step(k, lane, o, false);
-  return k;
-}
-// lists[0] becomes the 32 largest of n falling lists (n a power of two, at most
-// twice the block's warps).  Every thread of the block calls it.
-__device__ __forceinline__ void block_merge(unsigned long long (*lists)[32], int n, int warp,
-                                            int lane) {
-  for (int s = n / 2; s > 0; s /= 2) {
-    __syncthreads();
-    if (warp < s) {
-      const unsigned long long k = warp_merge(lists[warp][lane], lists[warp + s][31 - lane], lane);
-      lists[warp][lane] = k;
-    }
-  }
-  __syncthreads();
-}
+constexpr int kLpGroups = 64;           // groups of threads whose maxima bound the k-th element
+constexpr int kLpHits = 256;            // vectors that may hold candidates
+constexpr int kLpCandidates = 1024;     // at least 31 * 4 threads' vectors and 14 elements
 
-// The running best 32 of a warp: `best` falls over the lanes, `buf` holds up to
-// 63 keys that have not been sorted in yet.
-struct WarpTop {
-  unsigned long long best, *buf;
-  int n;
-  __device__ void flush(int lane) {
-    __syncwarp();
-    unsigned long long k = lane < n ? buf[lane] : 0ull;
-    unsigned long long rest = 32 + lane < n ? buf[32 + lane] : 0ull;
-    __syncwarp();
-    k = warp_sort(k, lane);
-    best = warp_merge(best, __shfl_sync(0xffffffffu, k, 31 - lane), lane);
-    n = n > 32 ? n - 32 : 0;
-    if (lane < n) buf[lane] = rest;
-    __syncwarp();
-  }
-  __device__ void add(unsigned long long k, bool take, int lane) {
-    const unsigned mask = __ballot_sync(0xffffffffu, take);
-    if (!mask) return;
-    if (take) buf[n + __popc(mask & ((1u << lane) - 1))] = k;
-    n += __popc(mask);
-    if (n >= 32) flush(lane);
-  }
+struct LpTop {
+  uint4 hit[kLpHits];
+  unsigned long long group[kLpGroups], least;
+  unsigned long long candidate[kLpCandidates], best[32];
+  int hit_at[kLpHits], hits, found;
 };
 
+// Largest of a key over `width` neighbouring lanes (a power of two).
+__device__ __forceinline__ unsigned long long key_max(unsigned long long k, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) {
+    const unsigned long long other = __shfl_xor_sync(0xffffffffu, k, o);
+    k = other > k ? other : k;
+  }
+  return k;
+}
+
+// How many of the n keys are above k, counted by `width` neighbouring lanes (a power
+// of two) that all call it with the same k; each gets the sum.
+__device__ __forceinline__ int key_rank(unsigned long long k, const unsigned long long *keys, int n,
+                                        int width, int lane) {
+  int above = 0;
+  for (int j = lane & (width - 1); j < n; j += width) above += keys[j] > k;
+  for (int o = width / 2; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+  return above;
+}
+
+// How many of a falling list's first n <= 32 keys are above k.
+__device__ __forceinline__ int key_rank_sorted(unsigned long long k, const unsigned long long *list, int n) {
+  int above = 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (above + o <= n && list[above + o - 1] > k) above += o;
+  return above + (above < n && list[above] > k);
+}
+
 // ------------------------------------------------------------- forward
-enum : int { kLpNone = -3, kLpHead = -2, kLpTail = -1 };
+constexpr int kLpNone = -1;             // no vector yet
 
 template <typename T, bool ENT, bool TOP>
 __global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
   constexpr int N = LpVec<T>::N;
   __shared__ LpSum warp_sum[kLpMaxWarps], rank_sum[kLpMaxCluster];
   __shared__ float final_stats[3];                           // m, ln Z, 1 if the row is bad
-  __shared__ unsigned long long lists[TOP ? kLpMaxWarps : 1][32];
-  __shared__ unsigned long long rank_top[TOP ? kLpMaxCluster : 1][32];
-  __shared__ unsigned long long bufs[TOP ? kLpMaxWarps : 1][64];
+  __shared__ std::conditional_t<TOP, LpTop, int> top[1];
+  __shared__ unsigned long long rank_top[TOP ? kLpMaxCluster * 32 : 1];
   cg::cluster_group cluster = cg::this_cluster();
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
-  const int cs = p.cluster, rank = cs > 1 ? blockIdx.x % cs : 0;
-  const long long row = blockIdx.x / cs;
+  const int cs = 1 << p.cluster_log2, rank = blockIdx.x & (cs - 1);
+  const long long row = blockIdx.x >> p.cluster_log2;
   if (cs > 1) cluster.barrier_arrive();
   const LpRow<T> R(static_cast<const T *>(p.logits) + row * p.ld, p.vocab);
   const uint4 *body = reinterpret_cast<const uint4 *>(R.body);
-  const int v_lo = (int)((long long)R.nvec * rank / cs);
-  const int v_hi = (int)((long long)R.nvec * (rank + 1) / cs);
+  const int per = (R.nvec + cs - 1) >> p.cluster_log2;
+  const int v_lo = min(per * rank, R.nvec), v_hi = min(v_lo + per, R.nvec);
   const bool has_head = rank == 0 && tid < R.head, has_tail = rank == cs - 1 && tid < R.tail;
   float x_target = 0.f;
   int target = -1;
@@ -241,45 +237,49 @@ __global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
     if (target >= 0 && target < p.vocab) x_target = LpVec<T>::to_f(R.row[target]);
   }
 
-  // one pass: running maximum, sums, and where the maximum was first seen
+  // one pass: running maximum, sums, and the first vector that holds the maximum
+  // (counted through the thread's vectors)
   LpSum a{-INFINITY, 0.f, 0.f};
   int seen = kLpNone;
-  auto one = [&](float x, int where) {
-    if (seen == kLpNone) seen = where;
-    if (x > a.m) {
-      lp_rescale(a, x);
-      seen = where;
-    }
-    lp_term<ENT>(x, a.m == -INFINITY ? 0.f : a.m, a.z, a.s);
-  };
-  if (has_head) one(LpVec<T>::to_f(R.row[tid]), kLpHead);
-  if (TOP && seen == kLpNone && v_lo + tid < v_hi) seen = 0;
-  int batch = 0;
-  for (int v = v_lo + tid; v < v_hi; v += nt * kLpBatch, ++batch) {
-    uint4 u[kLpBatch];
-    const uint32_t fill = minus_inf_bits<T>();
+  const float x_head = has_head ? LpVec<T>::to_f(R.row[tid]) : 0.f;
+  const float x_tail = has_tail ? LpVec<T>::to_f(R.row[R.tail_index() + tid]) : 0.f;
+  // full batches of kLpBatch vectors, then the rest one by one
+  int v = v_lo + tid;
+  auto add = [&](auto count) {
+    constexpr int B = decltype(count)::value;
+    uint4 u[B];
+    float vm[B], bm = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) {
-      u[i] = make_uint4(fill, fill, fill, fill);
-      if (v + i * nt < v_hi) u[i] = __ldg(body + v + i * nt);
-    }
-    float bm = vec_max<T>(u[0]);
+    for (int i = 0; i < B; ++i) u[i] = __ldg(body + v + i * nt);
 #pragma unroll
-    for (int i = 1; i < kLpBatch; ++i) bm = fmaxf(bm, vec_max<T>(u[i]));
-    if (bm > a.m) {
-      lp_rescale(a, bm);
-      seen = batch;
+    for (int i = 0; i < B; ++i) bm = fmaxf(bm, vm[i] = vec_max<T>(u[i]));
+    if (bm > a.m || (TOP && a.m == -INFINITY && seen == kLpNone)) {
+      if (bm > a.m) lp_rescale(a, bm);
+#pragma unroll
+      for (int i = B - 1; i >= 0; --i)
+        if (vm[i] == bm) seen = v + i * nt;
     }
     const float mr = a.m == -INFINITY ? 0.f : a.m;
+    float2 z = make_float2(a.z, 0.f), s = make_float2(a.s, 0.f);
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) {
+    for (int i = 0; i < B; ++i) {
       float f[N];
       LpVec<T>::unpack(u[i], f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) lp_term<ENT>(f[e], mr, a.z, a.s);
+      for (int e = 0; e < N; e += 2) lp_terms<ENT>(make_float2(f[e], f[e + 1]), mr, z, s);
     }
-  }
-  if (has_tail) one(LpVec<T>::to_f(R.row[R.tail_index() + tid]), kLpTail);
+    a.z = z.x + z.y;
+    a.s = s.x + s.y;
+  };
+  for (; v + (kLpBatch - 1) * nt < v_hi; v += nt * kLpBatch) add(std::integral_constant<int, kLpBatch>{});
+  for (; v < v_hi; v += nt) add(std::integral_constant<int, 1>{});
+  const float vector_max = a.m;
+  auto one = [&](float x) {
+    if (x > a.m) lp_rescale(a, x);
+    lp_term<ENT>(x, a.m == -INFINITY ? 0.f : a.m, a.z, a.s);
+  };
+  if (has_head) one(x_head);
+  if (has_tail) one(x_tail);
 
   // join the block's parts, then the cluster's in its first block
   LpSum t = a;
@@ -290,55 +290,99 @@ __global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
   if (lane == 0) warp_sum[warp] = t;
 
   if constexpr (TOP) {
-    // this thread's largest element, found again where it was seen
-    unsigned long long mine = 0;
-    if (seen == kLpHead) {
-      mine = lp_key(LpVec<T>::to_f(R.row[tid]), tid);
-    } else if (seen == kLpTail) {
-      mine = lp_key(LpVec<T>::to_f(R.row[R.tail_index() + tid]), R.tail_index() + tid);
-    } else if (seen >= 0) {
-      const int v0 = v_lo + tid + seen * nt * kLpBatch;
-#pragma unroll
-      for (int i = 0; i < kLpBatch; ++i) {
-        const int v = v0 + i * nt;
-        if (v >= v_hi) break;
-        float f[N];
-        LpVec<T>::unpack(__ldg(body + v), f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const unsigned long long k = lp_key(f[e], R.head + v * N + e);
-          mine = k > mine ? k : mine;
-        }
-      }
+    // `low` is at most the thread's largest key: it takes the last index of the
+    // vector that holds the maximum; `high`, with its first index, is at least the
+    // largest key of the thread's vectors
+    LpTop &S = top[0];
+    const unsigned long long kh = has_head ? lp_key(x_head, tid) : 0ull;
+    const unsigned long long kt = has_tail ? lp_key(x_tail, R.tail_index() + tid) : 0ull;
+    unsigned long long low = kh > kt ? kh : kt, high = 0;
+    if (seen != kLpNone) {
+      high = lp_key(vector_max, R.head + seen * N);
+      const unsigned long long l = lp_key(vector_max, R.head + seen * N + N - 1);
+      low = l > low ? l : low;
     }
-    lists[warp][lane] = warp_sort(mine, lane);
-    block_merge(lists, nw, warp, lane);
-    const unsigned long long least = lists[0][p.top_k - 1];
+    const int width = nt / kLpGroups;
+    const unsigned long long g = key_max(low, width);
+    if (tid % width == 0) S.group[tid / width] = g;
+    if (tid == 0) S.found = S.hits = 0;
     __syncthreads();
-    WarpTop top{0ull, bufs[warp], 0};
     {
-      unsigned long long k = has_head ? lp_key(LpVec<T>::to_f(R.row[tid]), tid) : 0ull;
-      top.add(k, k != 0 && k >= least, lane);
-      k = has_tail ? lp_key(LpVec<T>::to_f(R.row[R.tail_index() + tid]), R.tail_index() + tid) : 0ull;
-      top.add(k, k != 0 && k >= least, lane);
+      // (empty groups are all 0: the first of equals takes the place)
+      const int mine = tid / width;
+      const unsigned long long k = S.group[mine];
+      int rank = 0;
+      for (int j = tid % width; j < kLpGroups; j += width) rank += S.group[j] > k || (S.group[j] == k && j < mine);
+      for (int o = width / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (rank == p.top_k - 1) S.least = k;
     }
-    for (unsigned todo = __ballot_sync(0xffffffffu, mine != 0 && mine >= least); todo;
-         todo &= todo - 1) {
-      const int v0 = v_lo + warp * 32 + __ffs(todo) - 1;     // the first vector of that thread
-      for (int base = v0; base < v_hi; base += 32 * nt) {
-        const int v = base + lane * nt;
-        float f[N];
-        if (v < v_hi) LpVec<T>::unpack(__ldg(body + v), f);
+    __syncthreads();
+    while (true) {
+      const unsigned long long least = S.least;
+      auto offer = [&](unsigned long long k) {
+        if (k < least || k == 0) return;
+        const int at = atomicAdd(&S.found, 1);
+        if (at < kLpCandidates) S.candidate[at] = k;
+      };
+      offer(kh);
+      offer(kt);
+      // a warp reads the vectors of its threads that may hold candidates, four
+      // threads at a time
+      for (unsigned todo = __ballot_sync(0xffffffffu, high != 0 && high >= least); todo;) {
+        int of[4];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const unsigned long long k = v < v_hi ? lp_key(f[e], R.head + v * N + e) : 0ull;
-          top.add(k, k != 0 && k >= least, lane);
+        for (int i = 0; i < 4; ++i) {
+          of[i] = todo ? __ffs(todo) - 1 : v_hi;
+          todo &= todo - 1;
+        }
+        for (int base = v_lo + warp * 32 + lane * nt; base < v_hi; base += 32 * nt) {
+          uint4 u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (base + of[i] < v_hi) u[i] = __ldg(body + base + of[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = base + of[i];
+            if (at >= v_hi || lp_key(vec_max<T>(u[i]), R.head + at * N) < least) continue;
+            const int n = atomicAdd(&S.hits, 1);
+            if (n < kLpHits) {
+              S.hit[n] = u[i];
+              S.hit_at[n] = at;
+            }
+          }
         }
       }
+      __syncthreads();
+      // their elements, one a thread
+      const int hits = S.hits;
+      for (int i = tid; i < min(hits, kLpHits) * N; i += nt) {
+        const T x = reinterpret_cast<const T *>(&S.hit[i / N])[i % N];
+        offer(lp_key(LpVec<T>::to_f(x), R.head + S.hit_at[i / N] * N + i % N));
+      }
+      __syncthreads();
+      const int found = S.found, kept = min(found, kLpCandidates);
+      const bool whole = found <= kLpCandidates && hits <= kLpHits;
+      unsigned long long mine = 0;
+      const int share = nt / 32;                             // lanes for each candidate
+      for (int base = 0; base < kept; base += 32) {
+        const int i = base + tid / share;
+        const unsigned long long k = i < kept ? S.candidate[i] : ~0ull;
+        const int rank = key_rank(k, S.candidate, kept, share, lane);
+        if (i >= kept || tid % share) continue;
+        if (whole) {
+          if (rank < p.top_k) S.best[rank] = k;
+        } else if (rank == p.top_k - 1) {
+          mine = k;
+        }
+      }
+      __syncthreads();
+      if (whole) break;
+      // more than were kept: the k-th of those kept is a sharper bound (of kLpHits
+      // vectors all but one hold a candidate, so there is a k-th)
+      if (mine) S.least = mine;
+      if (tid == 0) S.found = S.hits = 0;
+      __syncthreads();
     }
-    if (top.n) top.flush(lane);
-    lists[warp][lane] = top.best;
-    block_merge(lists, nw, warp, lane);
   } else {
     __syncthreads();
   }
@@ -352,54 +396,67 @@ __global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
         w = lp_join(w, LpSum{__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.z, o),
                              __shfl_xor_sync(0xffffffffu, w.s, o)});
       if (lane == 0) *cluster.map_shared_rank(&rank_sum[rank], 0) = w;
-      if constexpr (TOP) *cluster.map_shared_rank(&rank_top[rank][lane], 0) = lists[0][lane];
+      if constexpr (TOP)
+        if (lane < p.top_k)
+          *cluster.map_shared_rank(&rank_top[rank * p.top_k + lane], 0) = top[0].best[lane];
     }
     cluster.sync();
     if (rank != 0) return;
-    if constexpr (TOP) block_merge(rank_top, cs, warp, lane);
   }
-  if (warp != 0) return;
-  const int parts = cs > 1 ? cs : nw;
-  LpSum w{-INFINITY, 0.f, 0.f};
-  if (lane < parts) w = cs > 1 ? rank_sum[lane] : warp_sum[lane];
+  if (warp == 0) {
+    const int parts = cs > 1 ? cs : nw;
+    LpSum w{-INFINITY, 0.f, 0.f};
+    if (lane < parts) w = cs > 1 ? rank_sum[lane] : warp_sum[lane];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
-    w = lp_join(w, LpSum{__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.z, o),
-                         __shfl_xor_sync(0xffffffffu, w.s, o)});
-  if (lane == 0) {
-    const float nan = __int_as_float(0x7FC00000);
-    const bool bad = !(w.z < INFINITY);                      // NaN or +inf among the logits
-    const bool empty = w.z == 0.f;                           // -inf alone
-    const float lz = bad ? nan : empty ? -INFINITY : logf(w.z);
-    if (p.logp) {
-      float lp = 0.f;
-      if (target >= p.vocab) {
-        set_device_error(kErrIndex);
-        lp = nan;
-      } else if (target >= 0) {
-        lp = bad ? nan : empty ? -INFINITY : (x_target - w.m) - lz;
+    for (int o = 8; o > 0; o >>= 1)
+      w = lp_join(w, LpSum{__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.z, o),
+                           __shfl_xor_sync(0xffffffffu, w.s, o)});
+    if (lane == 0) {
+      const float nan = __int_as_float(0x7FC00000);
+      const bool bad = !(w.z < INFINITY);                    // NaN or +inf among the logits
+      const bool empty = w.z == 0.f;                         // -inf alone
+      const float lz = bad ? nan : empty ? -INFINITY : logf(w.z);
+      if (p.logp) {
+        float lp = 0.f;
+        if (target >= p.vocab) {
+          set_device_error(kErrIndex);
+          lp = nan;
+        } else if (target >= 0) {
+          lp = bad ? nan : empty ? -INFINITY : (x_target - w.m) - lz;
+        }
+        p.logp[row] = lp;
       }
-      p.logp[row] = lp;
+      if (p.entropy) p.entropy[row] = bad ? nan : empty ? 0.f : lz - kLn2 * (w.s / w.z);
+      if (p.stats) {
+        p.stats[2 * row] = w.m;
+        p.stats[2 * row + 1] = lz;
+      }
+      final_stats[0] = w.m;
+      final_stats[1] = lz;
+      final_stats[2] = bad ? 1.f : empty ? 2.f : 0.f;
     }
-    if (p.entropy) p.entropy[row] = bad ? nan : empty ? 0.f : lz - kLn2 * (w.s / w.z);
-    if (p.stats) {
-      p.stats[2 * row] = w.m;
-      p.stats[2 * row + 1] = lz;
-    }
-    final_stats[0] = w.m;
-    final_stats[1] = lz;
-    final_stats[2] = bad ? 1.f : empty ? 2.f : 0.f;
   }
   if constexpr (TOP) {
-    __syncwarp();
-    if (lane < p.top_k) {
-      const unsigned long long k = cs > 1 ? rank_top[0][lane] : lists[0][lane];
-      const float kind = final_stats[2];
+    __syncthreads();
+    const float kind = final_stats[2];
+    auto put = [&](int place, unsigned long long k) {
       const float lp = kind == 1.f   ? __int_as_float(0x7FC00000)
                        : kind == 2.f ? -INFINITY
                                      : (lp_key_value(k) - final_stats[0]) - final_stats[1];
-      p.top_logp[row * p.top_k + lane] = lp;
-      p.top_id[row * p.top_k + lane] = kind == 1.f ? -1 : lp_key_index(k);
+      p.top_logp[row * p.top_k + place] = lp;
+      p.top_id[row * p.top_k + place] = kind == 1.f ? -1 : lp_key_index(k);
+    };
+    if (cs == 1) {
+      if (tid < p.top_k) put(tid, top[0].best[tid]);
+    } else {
+      for (int i = tid; i < cs * p.top_k; i += nt) {
+        const unsigned long long k = rank_top[i];
+        int place = 0;
+#pragma unroll
+        for (int r = 0; r < kLpMaxCluster; ++r)
+          if (r < cs) place += key_rank_sorted(k, rank_top + r * p.top_k, p.top_k);
+        if (place < p.top_k) put(place, k);
+      }
     }
   }
 }
@@ -417,15 +474,22 @@ __device__ __forceinline__ uint4 lp_pack(const float (&f)[LpVec<T>::N]) {
 template <typename T>
 __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   constexpr int N = LpVec<T>::N;
-  const long long row = blockIdx.x / p.parts;
-  const int part = (int)(blockIdx.x % p.parts), tid = threadIdx.x, nt = blockDim.x;
+  const long long row = blockIdx.x;
+  const int part = blockIdx.y, tid = threadIdx.x, nt = blockDim.x;
   const LpRow<T> R(static_cast<const T *>(p.logits) + row * p.ld, p.vocab);
   T *out = static_cast<T *>(p.dlogits) + row * p.ld;         // the same offset from 16 bytes
   const uint4 *src = reinterpret_cast<const uint4 *>(R.body);
   uint4 *dst = reinterpret_cast<uint4 *>(out + R.head);
-  const int v_lo = (int)((long long)R.nvec * part / p.parts);
-  const int v_hi = (int)((long long)R.nvec * (part + 1) / p.parts);
+  const int v_lo = min(part * p.per, R.nvec), v_hi = min(v_lo + p.per, R.nvec);
 
+  // the first vectors go out before the row's gradients are known
+  uint4 u[kLpBatch];
+  auto fetch = [&](int v) {
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i)
+      if (v + i * nt < v_hi) u[i] = src[v + i * nt];
+  };
+  fetch(v_lo + tid);
   int target = p.target ? __ldg(p.target + row) : -1;
   if (target >= p.vocab) {
     if (part == 0 && tid == 0) set_device_error(kErrIndex);
@@ -435,7 +499,7 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   const float de = p.dentropy ? __ldg(p.dentropy + row) : 0.f;
   const float m = __ldg(p.in_stats + 2 * row), lz = __ldg(p.in_stats + 2 * row + 1);
   const bool empty = lz == -INFINITY;                        // -inf alone: no gradient
-  const bool head = part == 0 && tid < R.head, tail = part == p.parts - 1 && tid < R.tail;
+  const bool head = part == 0 && tid < R.head, tail = part == (int)gridDim.y - 1 && tid < R.tail;
   if ((up == 0.f && de == 0.f) || empty) {
     if (head) out[tid] = T(0.f);
     for (int v = v_lo + tid; v < v_hi; v += nt) dst[v] = make_uint4(0, 0, 0, 0);
@@ -446,29 +510,35 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   // 0 all the same, so that -inf does not meet 0.  Rows with NaN have a NaN lz.
   float c1 = p.dentropy ? fmaf(de, __ldg(p.in_entropy + row), up) : up;
   if (lz != lz) c1 = lz;
-  auto grad = [&](float x) {
-    const float l = fmaxf((x - m) - lz, -1e4f);
-    return -ex2_approx(l * kLog2e) * fmaf(de, l, c1);
+  auto grad = [&](float2 x) {
+    float2 l = add2(add2(x, make_float2(-m, -m)), make_float2(-lz, -lz));
+    l.x = fmaxf(l.x, -1e4f);
+    l.y = fmaxf(l.y, -1e4f);
+    const float2 t = mul2(l, make_float2(kLog2e, kLog2e));
+    return mul2(make_float2(ex2_approx(t.x), ex2_approx(t.y)),
+                fma2(make_float2(-de, -de), l, make_float2(-c1, -c1)));
   };
   auto scalar = [&](int i) {
-    const float g = grad(LpVec<T>::to_f(R.row[i])) + (i == target ? up : 0.f);
+    const float x = LpVec<T>::to_f(R.row[i]);
+    const float g = grad(make_float2(x, x)).x + (i == target ? up : 0.f);
     if constexpr (sizeof(T) == 4) out[i] = g;
     else out[i] = Cvt<T>::from_f(g);
   };
   if (head) scalar(tid);
   const int tv = target >= R.head ? (target - R.head) / N : -1;     // the target's vector
   for (int v = v_lo + tid; v < v_hi; v += nt * kLpBatch) {
-    uint4 u[kLpBatch];
-#pragma unroll
-    for (int i = 0; i < kLpBatch; ++i)
-      if (v + i * nt < v_hi) u[i] = src[v + i * nt];
+    if (v != v_lo + tid) fetch(v);
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) {
       if (v + i * nt >= v_hi) break;
       float f[N];
       LpVec<T>::unpack(u[i], f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = grad(f[e]);
+      for (int e = 0; e < N; e += 2) {
+        const float2 g = grad(make_float2(f[e], f[e + 1]));
+        f[e] = g.x;
+        f[e + 1] = g.y;
+      }
       if (v + i * nt == tv) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -513,11 +583,11 @@ int launch_lp_fwd(const LpParams &p, unsigned grid, int threads, cudaStream_t st
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cluster;
+  at[0].val.clusterDim.x = 1u << p.cluster_log2;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  cfg.numAttrs = p.cluster_log2 > 0 ? 1 : 0;
   GPTL_CK(cudaLaunchKernelEx(&cfg, kern, p));
   return GPTL_OK;
 }
@@ -551,12 +621,13 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   // A row's blocks: 1 once the rows fill the SMs, else up to 8 of at least
   // 2048 elements each.
   int cs = 1;
-  while (cs < kLpMaxCluster && (long long)rows * cs * 2 <= 2ll * sms && vocab / (2 * cs) >= 2048)
+  while (cs < kLpMaxCluster && (long long)rows * cs < (long long)kLpFill * sms && vocab / (2 * cs) >= 2048) {
     cs *= 2;
-  p.cluster = cs;
+    ++p.cluster_log2;
+  }
   const int per_vec = logits_f32 ? 4 : 8;
   const int vecs = vocab / per_vec / cs;
-  const int threads = vecs >= 1024 ? 512 : vecs >= 256 ? 256 : 128;
+  const int threads = vecs >= 256 && (long long)rows * cs < (long long)kLpNarrow * sms ? 256 : 128;
   if ((long long)rows * cs >= (1ll << 31)) return GPTL_E_SHAPE;
   const unsigned grid = (unsigned)rows * (unsigned)cs;
   prof_start(st);
@@ -588,11 +659,12 @@ int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   p.dlogp = dlogp;
   p.dentropy = dentropy;
   p.dlogits = dlogits;
-  const int vecs = vocab / (logits_f32 ? 4 : 8);
-  p.parts = (vecs + 256 * kLpBatch - 1) / (256 * kLpBatch);
-  if (p.parts < 1) p.parts = 1;
-  if ((long long)rows * p.parts >= (1ll << 31)) return GPTL_E_SHAPE;
-  const unsigned grid = (unsigned)((long long)rows * p.parts);
+  // a row in even parts of at most kLpBatch vectors a thread, at most 65535 parts
+  const int vecs = vocab / (logits_f32 ? 4 : 8) + 1;
+  int parts = (vecs + 256 * kLpBatch - 1) / (256 * kLpBatch);
+  if (parts > 65535) parts = 65535;
+  p.per = (vecs + parts - 1) / parts;
+  const dim3 grid(rows, parts);
   prof_start(st);
   if (logits_f32) logprob_bwd_kernel<float><<<grid, 256, 0, st>>>(p);
   else if (dtype == GPTL_FP16) logprob_bwd_kernel<__half><<<grid, 256, 0, st>>>(p);
