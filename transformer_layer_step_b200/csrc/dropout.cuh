@@ -22,7 +22,8 @@
 
 namespace gptl {
 
-constexpr int kDropRows = 4;            // rows of a thread in flight
+constexpr int kDropRows = 2;            // rows of a thread in flight
+constexpr int kDropBlocksPerSm = 4;     // resident (64 registers a thread)
 
 struct DropParams {
   const void *in;                       // x or dy
@@ -136,7 +137,8 @@ __global__ void __launch_bounds__(256) dropout_fwd_kernel(const DropParams p) {
 }
 
 template <typename T, typename TD, bool SUM>
-__global__ void __launch_bounds__(256) dropout_bwd_kernel(const DropParams p) {
+__global__ void __launch_bounds__(256, kDropBlocksPerSm) dropout_bwd_kernel(const DropParams p) {
+  if constexpr (SUM) grid_dependents_launch();
   const int team = threadIdx.x / p.lanes, teams = blockDim.x / p.lanes;
   const int cv = blockIdx.x * p.lanes + threadIdx.x % p.lanes;
   const bool on = cv < p.h / 8;
@@ -186,13 +188,34 @@ __global__ void __launch_bounds__(256) dropout_bwd_kernel(const DropParams p) {
   }
 }
 
+// Adds the partial rows in order: 32 columns and 16 runs of rows a block.
+__global__ void __launch_bounds__(512) drop_bias_kernel(const float *__restrict__ part, int splits, int h,
+                                                        float *__restrict__ dbias) {
+  __shared__ float sm[16][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  grid_dependency_wait();
+  if (c < h) {
+#pragma unroll 4
+    for (int r = threadIdx.y; r < splits; r += 16) s += part[(long long)r * h + c];
+  }
+  sm[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < h) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sm[i][threadIdx.x];
+    dbias[c] = t;
+  }
+}
+
 __global__ void rng_advance_kernel(gptl_rng_state *rng, unsigned long long n) { rng->offset += n; }
 
 }  // namespace gptl
 
 namespace {
 
-constexpr int kDropBlocks = 8 * 148;      // blocks that a backward with dbias aims at
+constexpr int kDropBlocks = kDropBlocksPerSm * 148;   // blocks of a backward with dbias: one wave
 
 // Threads side by side on a row (a power of two, at most a warp), and the
 // strips of that many vectors that cover it.
@@ -211,8 +234,8 @@ int drop_splits(int rows, int h, bool sums) {
   const int strips = (h / 8 + lanes - 1) / lanes;
   long long most = ((long long)rows + teams * kDropRows - 1) / (teams * kDropRows);
   if (sums) {
-    const long long want = (kDropBlocks + strips - 1) / strips;
-    if (most > want) most = want;
+    const long long want = kDropBlocks / strips;
+    if (most > want) most = want > 0 ? want : 1;
   }
   return (int)(most > 65535 ? 65535 : most);
 }
@@ -325,7 +348,10 @@ int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int 
   GPTL_CK(cudaGetLastError());
   prof_launched(st, GPTL_KIND_DROPOUT_BWD);
   if (!dbias) return GPTL_OK;
-  return launch_reduce_parts(a.part, splits, h, 1, dbias, nullptr, nullptr, nullptr, st);
+  GPTL_TRY(launch_after(drop_bias_kernel, dim3((h + 31) / 32), dim3(32, 16), st, (const float *)a.part,
+                        splits, h, dbias));
+  prof_launched(st, GPTL_KIND_REDUCE);
+  return GPTL_OK;
 }
 
 }  // extern "C"

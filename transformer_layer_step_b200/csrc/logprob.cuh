@@ -42,6 +42,8 @@ namespace cg = cooperative_groups;
 constexpr int kLpMaxWarps = 16;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpFill = 1, kLpNarrow = 8;
+constexpr int kLpBwdVecs = 32, kLpBwdWarps = 64;
+constexpr int kLpWarpVecs = 256;        // longest row of a warp, in vectors
 constexpr int kLpBatch = 4;             // 16-byte loads of a thread in flight
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
@@ -56,7 +58,7 @@ struct LpParams {
   // backward
   const float *in_stats, *in_entropy, *dlogp, *dentropy;
   void *dlogits;
-  int per;                              // vectors of a block
+  int per;                              // vectors of a part
 };
 
 // ------------------------------------------------------- 16-byte vectors
@@ -213,17 +215,21 @@ __device__ __forceinline__ int key_rank_sorted(unsigned long long k, const unsig
 // ------------------------------------------------------------- forward
 constexpr int kLpNone = -1;             // no vector yet
 
-template <typename T, bool ENT, bool TOP>
-__global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
+// WARP: a warp takes a row, for short rows; else a block or a cluster does.
+template <typename T, bool ENT, bool TOP, bool WARP>
+__global__ void __launch_bounds__(256, TOP ? 4 : 5) logprob_fwd_kernel(const LpParams p) {
+  static_assert(!(TOP && WARP), "the alternatives take a block");
   constexpr int N = LpVec<T>::N;
   __shared__ LpSum warp_sum[kLpMaxWarps], rank_sum[kLpMaxCluster];
   __shared__ float final_stats[3];                           // m, ln Z, 1 if the row is bad
   __shared__ std::conditional_t<TOP, LpTop, int> top[1];
   __shared__ unsigned long long rank_top[TOP ? kLpMaxCluster * 32 : 1];
   cg::cluster_group cluster = cg::this_cluster();
-  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
-  const int cs = 1 << p.cluster_log2, rank = blockIdx.x & (cs - 1);
-  const long long row = blockIdx.x >> p.cluster_log2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x / 32;
+  const int nt = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
+  const int cs = WARP ? 1 : 1 << p.cluster_log2, rank = blockIdx.x & (cs - 1);
+  const long long row = WARP ? (long long)blockIdx.x * nw + warp : blockIdx.x >> p.cluster_log2;
+  if (WARP && row >= p.rows) return;
   if (cs > 1) cluster.barrier_arrive();
   const LpRow<T> R(static_cast<const T *>(p.logits) + row * p.ld, p.vocab);
   const uint4 *body = reinterpret_cast<const uint4 *>(R.body);
@@ -287,6 +293,35 @@ __global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
   for (int o = 16; o > 0; o >>= 1)
     t = lp_join(t, LpSum{__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.z, o),
                          __shfl_xor_sync(0xffffffffu, t.s, o)});
+  // the row's results from its sums, by one thread
+  auto finish = [&](const LpSum &w) {
+    const float nan = __int_as_float(0x7FC00000);
+    const bool bad = !(w.z < INFINITY);                    // NaN or +inf among the logits
+    const bool empty = w.z == 0.f;                         // -inf alone
+    const float lz = bad ? nan : empty ? -INFINITY : logf(w.z);
+    if (p.logp) {
+      float lp = 0.f;
+      if (target >= p.vocab) {
+        set_device_error(kErrIndex);
+        lp = nan;
+      } else if (target >= 0) {
+        lp = bad ? nan : empty ? -INFINITY : (x_target - w.m) - lz;
+      }
+      p.logp[row] = lp;
+    }
+    if (p.entropy) p.entropy[row] = bad ? nan : empty ? 0.f : lz - kLn2 * (w.s / w.z);
+    if (p.stats) {
+      p.stats[2 * row] = w.m;
+      p.stats[2 * row + 1] = lz;
+    }
+    final_stats[0] = w.m;
+    final_stats[1] = lz;
+    final_stats[2] = bad ? 1.f : empty ? 2.f : 0.f;
+  };
+  if constexpr (WARP) {
+    if (lane == 0) finish(t);
+    return;
+  }
   if (lane == 0) warp_sum[warp] = t;
 
   if constexpr (TOP) {
@@ -411,30 +446,7 @@ __global__ void __launch_bounds__(512) logprob_fwd_kernel(const LpParams p) {
     for (int o = 8; o > 0; o >>= 1)
       w = lp_join(w, LpSum{__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.z, o),
                            __shfl_xor_sync(0xffffffffu, w.s, o)});
-    if (lane == 0) {
-      const float nan = __int_as_float(0x7FC00000);
-      const bool bad = !(w.z < INFINITY);                    // NaN or +inf among the logits
-      const bool empty = w.z == 0.f;                         // -inf alone
-      const float lz = bad ? nan : empty ? -INFINITY : logf(w.z);
-      if (p.logp) {
-        float lp = 0.f;
-        if (target >= p.vocab) {
-          set_device_error(kErrIndex);
-          lp = nan;
-        } else if (target >= 0) {
-          lp = bad ? nan : empty ? -INFINITY : (x_target - w.m) - lz;
-        }
-        p.logp[row] = lp;
-      }
-      if (p.entropy) p.entropy[row] = bad ? nan : empty ? 0.f : lz - kLn2 * (w.s / w.z);
-      if (p.stats) {
-        p.stats[2 * row] = w.m;
-        p.stats[2 * row + 1] = lz;
-      }
-      final_stats[0] = w.m;
-      final_stats[1] = lz;
-      final_stats[2] = bad ? 1.f : empty ? 2.f : 0.f;
-    }
+    if (lane == 0) finish(w);
   }
   if constexpr (TOP) {
     __syncthreads();
@@ -471,23 +483,26 @@ __device__ __forceinline__ uint4 lp_pack(const float (&f)[LpVec<T>::N]) {
     return pack8<T>(f);
 }
 
+// A warp takes a part of a row.
 template <typename T>
 __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   constexpr int N = LpVec<T>::N;
-  const long long row = blockIdx.x;
-  const int part = blockIdx.y, tid = threadIdx.x, nt = blockDim.x;
+  const int nt = 32, tid = threadIdx.x & 31, part = blockIdx.y;
+  const long long row = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  if (row >= p.rows) return;
   const LpRow<T> R(static_cast<const T *>(p.logits) + row * p.ld, p.vocab);
   T *out = static_cast<T *>(p.dlogits) + row * p.ld;         // the same offset from 16 bytes
   const uint4 *src = reinterpret_cast<const uint4 *>(R.body);
   uint4 *dst = reinterpret_cast<uint4 *>(out + R.head);
   const int v_lo = min(part * p.per, R.nvec), v_hi = min(v_lo + p.per, R.nvec);
 
-  // the first vectors go out before the row's gradients are known
-  uint4 u[kLpBatch];
+  // the first vectors go out before the row's gradients are known, and each
+  // batch before the one ahead of it is computed
+  uint4 next[kLpBatch];
   auto fetch = [&](int v) {
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i)
-      if (v + i * nt < v_hi) u[i] = src[v + i * nt];
+      if (v + i * nt < v_hi) next[i] = src[v + i * nt];
   };
   fetch(v_lo + tid);
   int target = p.target ? __ldg(p.target + row) : -1;
@@ -527,7 +542,10 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   if (head) scalar(tid);
   const int tv = target >= R.head ? (target - R.head) / N : -1;     // the target's vector
   for (int v = v_lo + tid; v < v_hi; v += nt * kLpBatch) {
-    if (v != v_lo + tid) fetch(v);
+    uint4 u[kLpBatch];
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i) u[i] = next[i];
+    fetch(v + nt * kLpBatch);
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) {
       if (v + i * nt >= v_hi) break;
@@ -572,11 +590,13 @@ int check_lp(int rows, int vocab, long long ld, gptl_dtype dt, int f32, const vo
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 template <typename T>
-int launch_lp_fwd(const LpParams &p, unsigned grid, int threads, cudaStream_t st) {
-  auto kern = p.top_k ? (p.entropy ? logprob_fwd_kernel<T, true, true>
-                                   : logprob_fwd_kernel<T, false, true>)
-                      : (p.entropy ? logprob_fwd_kernel<T, true, false>
-                                   : logprob_fwd_kernel<T, false, false>);
+int launch_lp_fwd(const LpParams &p, bool warp_rows, unsigned grid, int threads, cudaStream_t st) {
+  auto kern = p.top_k ? (p.entropy ? logprob_fwd_kernel<T, true, true, false>
+                                   : logprob_fwd_kernel<T, false, true, false>)
+              : warp_rows ? (p.entropy ? logprob_fwd_kernel<T, true, false, true>
+                                       : logprob_fwd_kernel<T, false, false, true>)
+                          : (p.entropy ? logprob_fwd_kernel<T, true, false, false>
+                                       : logprob_fwd_kernel<T, false, false, false>);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -625,15 +645,15 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
     cs *= 2;
     ++p.cluster_log2;
   }
-  const int per_vec = logits_f32 ? 4 : 8;
-  const int vecs = vocab / per_vec / cs;
-  const int threads = vecs >= 256 && (long long)rows * cs < (long long)kLpNarrow * sms ? 256 : 128;
+  const int vecs = vocab / (logits_f32 ? 4 : 8) / cs;
+  const bool warp_rows = top_k == 0 && (vecs <= kLpWarpVecs || (vecs <= 4 * kLpWarpVecs && rows >= 8 * sms));
+  const int threads = !warp_rows && vecs >= 256 && (long long)rows * cs < (long long)kLpNarrow * sms ? 256 : 128;
   if ((long long)rows * cs >= (1ll << 31)) return GPTL_E_SHAPE;
-  const unsigned grid = (unsigned)rows * (unsigned)cs;
+  const unsigned grid = warp_rows ? (unsigned)((rows + 3ll) / 4) : (unsigned)rows * (unsigned)cs;
   prof_start(st);
-  if (logits_f32) GPTL_TRY(launch_lp_fwd<float>(p, grid, threads, st));
-  else if (dtype == GPTL_FP16) GPTL_TRY(launch_lp_fwd<__half>(p, grid, threads, st));
-  else GPTL_TRY(launch_lp_fwd<__nv_bfloat16>(p, grid, threads, st));
+  if (logits_f32) GPTL_TRY(launch_lp_fwd<float>(p, warp_rows, grid, threads, st));
+  else if (dtype == GPTL_FP16) GPTL_TRY(launch_lp_fwd<__half>(p, warp_rows, grid, threads, st));
+  else GPTL_TRY(launch_lp_fwd<__nv_bfloat16>(p, warp_rows, grid, threads, st));
   prof_launched(st, GPTL_KIND_LOGPROB_FWD);
   return GPTL_OK;
 }
@@ -652,19 +672,25 @@ int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
     return GPTL_E_ALIGN;
   const long long bytes = ((rows - 1) * ld + vocab) * (logits_f32 ? 4 : 2);
   if (dlogits != logits && ranges_overlap(logits, bytes, dlogits, bytes)) return GPTL_E_ARG;
-  GPTL_TRY(device_check());
+  int sms = 0;
+  GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   p.in_stats = stats;
   p.in_entropy = entropy;
   p.dlogp = dlogp;
   p.dentropy = dentropy;
   p.dlogits = dlogits;
-  // a row in even parts of at most kLpBatch vectors a thread, at most 65535 parts
+  // A warp's part of a row: as long as leaves kLpBwdWarps warps an SM, so that the
+  // row's scalars and the first loads are small beside it, but at most kLpBwdVecs
+  // vectors a lane, and one batch at least.
   const int vecs = vocab / (logits_f32 ? 4 : 8) + 1;
-  int parts = (vecs + 256 * kLpBatch - 1) / (256 * kLpBatch);
+  long long lane_vecs = (long long)rows * vecs / (32ll * kLpBwdWarps * sms);
+  if (lane_vecs > kLpBwdVecs) lane_vecs = kLpBwdVecs;
+  if (lane_vecs < kLpBatch) lane_vecs = kLpBatch;
+  int parts = (int)((vecs + 32 * lane_vecs - 1) / (32 * lane_vecs));
   if (parts > 65535) parts = 65535;
   p.per = (vecs + parts - 1) / parts;
-  const dim3 grid(rows, parts);
+  const dim3 grid((unsigned)((rows + 7ll) / 8), parts);
   prof_start(st);
   if (logits_f32) logprob_bwd_kernel<float><<<grid, 256, 0, st>>>(p);
   else if (dtype == GPTL_FP16) logprob_bwd_kernel<__half><<<grid, 256, 0, st>>>(p);
