@@ -248,3 +248,54 @@ def test_graph_replay_and_side_stream():
     want = _check_fwd(o, y, t_t.cpu().numpy(), 12)
     one = np.ones(rows, np.float32)
     _check_bwd(d_t[:rows].double().cpu().numpy(), y, t_t.cpu().numpy(), one, one, want, "bf16")
+
+
+def _ordered_rows(kind, rows, vocab, dtype):
+    """Rows that crowd the search for the top: far more elements than are kept in
+    the vectors of a few threads, slopes, plateaus and one repeated value."""
+    i = torch.arange(vocab, dtype=torch.float64)
+    if kind == "crowd":                     # 20 of every 256 vectors hold everything large
+        x = torch.where((i // (16 // TORCH[dtype].itemsize)) % 256 < 20, 5 + i / vocab, -i / vocab)
+    elif kind == "rising":
+        x = i / 64
+    elif kind == "falling":
+        x = -i / 64
+    elif kind == "plateau":                 # half of the row shares the largest value
+        x = torch.where(i % 2 == 1, 3.0, 1.0)
+    else:                                   # "same"
+        x = torch.full((vocab,), -7.0, dtype=torch.float64)
+    return x.expand(rows, -1).to(TORCH[dtype]).contiguous()
+
+
+@pytest.mark.parametrize("kind", ["crowd", "rising", "falling", "plateau", "same"])
+@pytest.mark.parametrize("dtype,rows,vocab,pad,top_k", [
+    ("bf16", 150, 40000, 0, 32), ("fp32", 150, 21001, 0, 20), ("fp16", 1200, 12001, 1, 32),
+    ("bf16", 2, 70003, 0, 32), ("fp32", 3, 9000, 1, 1), ("fp16", 2, 1030, 0, 32)])
+def test_top_of_ordered_rows(kind, dtype, rows, vocab, pad, top_k):
+    """One block a row, and a cluster, where candidates overflow what is kept, tie
+    over half of the row, or lie in one thread's vectors."""
+    need_gpu()
+    x = _ordered_rows(kind, rows, vocab, dtype)
+    x_t = torch.full((rows, vocab + pad), 1e4, dtype=x.dtype, device="cuda")
+    x_t[:, :vocab] = x.cuda()
+    o = _fwd(x_t, rows, vocab, vocab + pad, dtype, None, top_k)
+    check_device_error()
+    want = parts.token_logprob_fwd(x[:1].double().numpy(), None, top_k)
+    ids = o["top_id"].cpu().numpy()
+    assert (ids == want["top_id"]).all(), ids[(ids != want["top_id"]).any(1)][:1]
+    _check_fwd({k: None if v is None else v[:1] for k, v in o.items()}, x[:1].double().numpy(), None, top_k)
+
+
+def test_two_streams_at_once():
+    need_gpu()
+    rows, vocab = 4, 50001
+    sides = []
+    for k in range(2):
+        x_t, x = _logits(rows, vocab, vocab, "bf16", 20 + k)
+        sides.append((x_t, x, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[_fwd(x_t, rows, vocab, vocab, "bf16", None, 8, st.cuda_stream) for x_t, _, st in sides] for _ in range(20)]
+    check_device_error()
+    for pair in outs:
+        for o, (_, x, _) in zip(pair, sides):
+            _check_fwd(o, x, None, 8)
