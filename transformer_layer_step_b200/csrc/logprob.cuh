@@ -41,10 +41,11 @@ namespace cg = cooperative_groups;
 
 constexpr int kLpMaxWarps = 16;
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpFill = 1, kLpNarrow = 8;
+constexpr int kLpFill = 1, kLpNarrow = 5;
 constexpr int kLpBwdVecs = 32, kLpBwdWarps = 64;
 constexpr int kLpWarpVecs = 256;        // longest row of a warp, in vectors
-constexpr int kLpBatch = 4;             // 16-byte loads of a thread in flight
+constexpr int kLpBatch = 4;             // 16-byte loads of a thread in a batch
+constexpr int kLpShortBatch = 2;        // the same where a warp takes a short row
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
 struct LpParams {
@@ -217,7 +218,7 @@ constexpr int kLpNone = -1;             // no vector yet
 
 // WARP: a warp takes a row, for short rows; else a block or a cluster does.
 template <typename T, bool ENT, bool TOP, bool WARP>
-__global__ void __launch_bounds__(256, TOP ? 4 : 5) logprob_fwd_kernel(const LpParams p) {
+__global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const LpParams p) {
   static_assert(!(TOP && WARP), "the alternatives take a block");
   constexpr int N = LpVec<T>::N;
   __shared__ LpSum warp_sum[kLpMaxWarps], rank_sum[kLpMaxCluster];
@@ -249,26 +250,25 @@ __global__ void __launch_bounds__(256, TOP ? 4 : 5) logprob_fwd_kernel(const LpP
   int seen = kLpNone;
   const float x_head = has_head ? LpVec<T>::to_f(R.row[tid]) : 0.f;
   const float x_tail = has_tail ? LpVec<T>::to_f(R.row[R.tail_index() + tid]) : 0.f;
-  // full batches of kLpBatch vectors, then the rest one by one
+  // full batches of B vectors, each loaded while the one before it is
+  // added, then the rest one by one
+  constexpr int B = WARP ? kLpShortBatch : kLpBatch;
   int v = v_lo + tid;
-  auto add = [&](auto count) {
-    constexpr int B = decltype(count)::value;
-    uint4 u[B];
+  auto add = [&](const auto &u) {
+    constexpr int M = sizeof(u) / sizeof(uint4);
     float vm[B], bm = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < B; ++i) u[i] = __ldg(body + v + i * nt);
-#pragma unroll
-    for (int i = 0; i < B; ++i) bm = fmaxf(bm, vm[i] = vec_max<T>(u[i]));
+    for (int i = 0; i < M; ++i) bm = fmaxf(bm, vm[i] = vec_max<T>(u[i]));
     if (bm > a.m || (TOP && a.m == -INFINITY && seen == kLpNone)) {
       if (bm > a.m) lp_rescale(a, bm);
 #pragma unroll
-      for (int i = B - 1; i >= 0; --i)
+      for (int i = M - 1; i >= 0; --i)
         if (vm[i] == bm) seen = v + i * nt;
     }
     const float mr = a.m == -INFINITY ? 0.f : a.m;
     float2 z = make_float2(a.z, 0.f), s = make_float2(a.s, 0.f);
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
+    for (int i = 0; i < M; ++i) {
       float f[N];
       LpVec<T>::unpack(u[i], f);
 #pragma unroll
@@ -277,8 +277,24 @@ __global__ void __launch_bounds__(256, TOP ? 4 : 5) logprob_fwd_kernel(const LpP
     a.z = z.x + z.y;
     a.s = s.x + s.y;
   };
-  for (; v + (kLpBatch - 1) * nt < v_hi; v += nt * kLpBatch) add(std::integral_constant<int, kLpBatch>{});
-  for (; v < v_hi; v += nt) add(std::integral_constant<int, 1>{});
+  const int last = v_hi - (B - 1) * nt;               // a batch may start before it
+  uint4 next[B];
+#pragma unroll
+  for (int i = 0; i < B; ++i)
+    if (v < last) next[i] = __ldg(body + v + i * nt);
+  for (; v < last; v += nt * B) {
+    uint4 u[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      u[i] = next[i];
+      if (v + nt * B < last) next[i] = __ldg(body + v + (B + i) * nt);
+    }
+    add(u);
+  }
+  for (; v < v_hi; v += nt) {
+    const uint4 u[1] = {__ldg(body + v)};
+    add(u);
+  }
   const float vector_max = a.m;
   auto one = [&](float x) {
     if (x > a.m) lp_rescale(a, x);
@@ -483,8 +499,8 @@ __device__ __forceinline__ uint4 lp_pack(const float (&f)[LpVec<T>::N]) {
     return pack8<T>(f);
 }
 
-// A warp takes a part of a row.
-template <typename T>
+// A warp takes a part of a row, in batches of B vectors a lane.
+template <typename T, int B>
 __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   constexpr int N = LpVec<T>::N;
   const int nt = 32, tid = threadIdx.x & 31, part = blockIdx.y;
@@ -498,10 +514,10 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
 
   // the first vectors go out before the row's gradients are known, and each
   // batch before the one ahead of it is computed
-  uint4 next[kLpBatch];
+  uint4 next[B];
   auto fetch = [&](int v) {
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i)
+    for (int i = 0; i < B; ++i)
       if (v + i * nt < v_hi) next[i] = src[v + i * nt];
   };
   fetch(v_lo + tid);
@@ -541,13 +557,13 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LpParams p) {
   };
   if (head) scalar(tid);
   const int tv = target >= R.head ? (target - R.head) / N : -1;     // the target's vector
-  for (int v = v_lo + tid; v < v_hi; v += nt * kLpBatch) {
-    uint4 u[kLpBatch];
+  for (int v = v_lo + tid; v < v_hi; v += nt * B) {
+    uint4 u[B];
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) u[i] = next[i];
-    fetch(v + nt * kLpBatch);
+    for (int i = 0; i < B; ++i) u[i] = next[i];
+    fetch(v + nt * B);
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) {
+    for (int i = 0; i < B; ++i) {
       if (v + i * nt >= v_hi) break;
       float f[N];
       LpVec<T>::unpack(u[i], f);
@@ -692,9 +708,13 @@ int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   p.per = (vecs + parts - 1) / parts;
   const dim3 grid((unsigned)((rows + 7ll) / 8), parts);
   prof_start(st);
-  if (logits_f32) logprob_bwd_kernel<float><<<grid, 256, 0, st>>>(p);
-  else if (dtype == GPTL_FP16) logprob_bwd_kernel<__half><<<grid, 256, 0, st>>>(p);
-  else logprob_bwd_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+  auto go = [&]<typename T>() {
+    if (p.per <= 32 * 2 * kLpBatch) logprob_bwd_kernel<T, kLpShortBatch><<<grid, 256, 0, st>>>(p);
+    else logprob_bwd_kernel<T, kLpBatch><<<grid, 256, 0, st>>>(p);
+  };
+  if (logits_f32) go.template operator()<float>();
+  else if (dtype == GPTL_FP16) go.template operator()<__half>();
+  else go.template operator()<__nv_bfloat16>();
   GPTL_CK(cudaGetLastError());
   prof_launched(st, GPTL_KIND_LOGPROB_BWD);
   return GPTL_OK;
