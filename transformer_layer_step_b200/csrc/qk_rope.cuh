@@ -172,22 +172,29 @@ __device__ __forceinline__ void qk_head_sum(const QkParams &p, int lane, int c, 
   }
 }
 
-// The value heads of the last blocks: a warp copies every v_warps-th row.
+// The value heads of the last blocks: a warp copies every v_warps-th row, four at
+// a time.
 template <typename T>
 __device__ void qk_copy_values(const QkParams &p, const T *from, long long f_ld, long long f_gs, T *to) {
   const int lane = threadIdx.x & 31;
-  const unsigned warps = p.v_blocks * kQkWarps;
-  const unsigned rows = (unsigned)p.tokens * p.groups;
-  for (unsigned r = (blockIdx.x - p.blocks_qk) * kQkWarps + threadIdx.x / 32; r < rows; r += warps) {
-    const unsigned g = r / p.tokens, t = r - g * p.tokens;
-    const uint4 *src = reinterpret_cast<const uint4 *>(from + g * f_gs + t * f_ld) + p.v_first;
-    uint4 *dst = reinterpret_cast<uint4 *>(to + g * p.y_gs + t * p.y_ld) + p.v_first;
-    int i = lane;
-    for (; i + 96 < p.v_vecs; i += 128) {
-      const uint4 a = src[i], b = src[i + 32], c = src[i + 64], d = src[i + 96];
-      dst[i] = a; dst[i + 32] = b; dst[i + 64] = c; dst[i + 96] = d;
+  const unsigned warps = p.v_blocks * kQkWarps, rows = (unsigned)p.tokens * p.groups;
+  for (unsigned r0 = (blockIdx.x - p.blocks_qk) * kQkWarps + threadIdx.x / 32; r0 < rows; r0 += 4 * warps) {
+    const uint4 *src[4];
+    uint4 *dst[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned r = r0 + k * warps < rows ? r0 + k * warps : r0;       // r0 again: the same bits
+      const unsigned g = r / p.tokens, t = r - g * p.tokens;
+      src[k] = reinterpret_cast<const uint4 *>(from + g * f_gs + t * f_ld) + p.v_first;
+      dst[k] = reinterpret_cast<uint4 *>(to + g * p.y_gs + t * p.y_ld) + p.v_first;
     }
-    for (; i < p.v_vecs; i += 32) dst[i] = src[i];
+    for (int i = lane; i < p.v_vecs; i += 32) {
+      uint4 u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = src[k][i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dst[k][i] = u[k];
+    }
   }
 }
 
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBloc
     const T *pd = in_dy + g0 * p.y_gs + token * p.y_ld + col;
     T *po = out + g0 * p.y_gs + token * p.y_ld + col, *o = po;
     uint4 nx0, nx1, nd0, nd1;
-    bool live, here;
+    bool live;
     auto fetch = [&]() {
       live = on && n < all;
       o = po;
@@ -292,68 +299,69 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBloc
     fetch();
     if (p.rot) qk_angles(p, turns_all, token, cs_all[warp], lane);
     for (int u = 0; u < n_slots; ++u) {
-      {
-        const uint4 x0 = nx0, x1 = nx1, d0 = nd0, d1 = nd1;
-        T *to = o;
-        here = live;
-        if (u + 1 < n_slots) fetch();                      // the next slot's loads go out first
-        float2 a[4], b[4];
+      // the slot's values leave the registers that the next slot's are loaded into
+      float2 a[4], b[4], xa[4], xb[4];
+      if constexpr (kX) qk_unpack<T, INTER>(nx0, nx1, xa, xb);
+      if constexpr (BWD) qk_unpack<T, INTER>(nd0, nd1, a, b);
+      T *to = o;
+      const bool here = live;
+      if (u + 1 < n_slots) fetch();
+      if constexpr (BWD)
+        if (turns) qk_turn<true>(a, b, cs, LPH);
+      if constexpr (NORM) {
+        float2 s2 = make_float2(0.f, 0.f), d2 = s2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = fma2(xa[i], xa[i], fma2(xb[i], xb[i], s2));
+        float ss = s2.x + s2.y, sd = 0.f;
         if constexpr (BWD) {
-          qk_unpack<T, INTER>(d0, d1, a, b);
-          if (turns) qk_turn<true>(a, b, cs, LPH);
-        }
-        if constexpr (NORM) {
-          float2 xa[4], xb[4], s2 = make_float2(0.f, 0.f), d2 = s2;
-          qk_unpack<T, INTER>(x0, x1, xa, xb);
+          // the gain's gradient takes dn x, then dn becomes d = dn g
+          float2 ta[4], tb[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s2 = fma2(xa[i], xa[i], fma2(xb[i], xb[i], s2));
-          float ss = s2.x + s2.y, sd = 0.f;
-          if constexpr (BWD) {
-            // the gain's gradient takes dn x, then dn becomes d = dn g
-            float2 ta[4], tb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 g = gain[i * LPH];
-              const float2 ga = make_float2(g.x, g.y), gb = make_float2(g.z, g.w);
-              ta[i] = mul2(a[i], xa[i]);
-              tb[i] = mul2(b[i], xb[i]);
-              d2 = fma2(ta[i], ga, fma2(tb[i], gb, d2));
-              a[i] = mul2(a[i], ga);
-              b[i] = mul2(b[i], gb);
-            }
-            sd = d2.x + d2.y;
-            qk_head_sum<LANES, true>(p, lane, c, ss, sd);
-            const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-            const float m = -r * r * r * (sd * p.inv_hd);
-            const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              acc_a[i] = fma2(ta[i], r2, acc_a[i]);
-              acc_b[i] = fma2(tb[i], r2, acc_b[i]);
-              a[i] = fma2(a[i], r2, mul2(xa[i], m2));
-              b[i] = fma2(b[i], r2, mul2(xb[i], m2));
-            }
-          } else {
-            qk_head_sum<LANES, false>(p, lane, c, ss, sd);
-            const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-            const float2 r2 = make_float2(r, r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 g = gain[i * LPH];
-              a[i] = mul2(mul2(xa[i], r2), make_float2(g.x, g.y));
-              b[i] = mul2(mul2(xb[i], r2), make_float2(g.z, g.w));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float4 g = gain[i * LPH];
+            const float2 ga = make_float2(g.x, g.y), gb = make_float2(g.z, g.w);
+            ta[i] = mul2(a[i], xa[i]);
+            tb[i] = mul2(b[i], xb[i]);
+            d2 = fma2(ta[i], ga, fma2(tb[i], gb, d2));
+            a[i] = mul2(a[i], ga);
+            b[i] = mul2(b[i], gb);
           }
-        } else if constexpr (!BWD) {
-          qk_unpack<T, INTER>(x0, x1, a, b);
+          sd = d2.x + d2.y;
+          qk_head_sum<LANES, true>(p, lane, c, ss, sd);
+          const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+          const float m = -r * r * r * (sd * p.inv_hd);
+          const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc_a[i] = fma2(ta[i], r2, acc_a[i]);
+            acc_b[i] = fma2(tb[i], r2, acc_b[i]);
+            a[i] = fma2(a[i], r2, mul2(xa[i], m2));
+            b[i] = fma2(b[i], r2, mul2(xb[i], m2));
+          }
+        } else {
+          qk_head_sum<LANES, false>(p, lane, c, ss, sd);
+          const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+          const float2 r2 = make_float2(r, r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 g = gain[i * LPH];
+            a[i] = mul2(mul2(xa[i], r2), make_float2(g.x, g.y));
+            b[i] = mul2(mul2(xb[i], r2), make_float2(g.z, g.w));
+          }
         }
-        if (!BWD && turns) qk_turn<false>(a, b, cs, LPH);
-        if (here) {
-          uint4 q0, q1;
-          qk_pack<T, INTER>(a, b, q0, q1);
-          *reinterpret_cast<uint4 *>(to) = q0;
-          *reinterpret_cast<uint4 *>(to + dv) = q1;
+      } else if constexpr (!BWD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = xa[i];
+          b[i] = xb[i];
         }
+      }
+      if (!BWD && turns) qk_turn<false>(a, b, cs, LPH);
+      if (here) {
+        uint4 q0, q1;
+        qk_pack<T, INTER>(a, b, q0, q1);
+        *reinterpret_cast<uint4 *>(to) = q0;
+        *reinterpret_cast<uint4 *>(to + dv) = q1;
       }
     }
   }
@@ -522,8 +530,8 @@ QkParams qk_params(const gptl_qk_desc &d, int v_heads, int blocks) {
   p.v_vecs = v_heads * d.head_dim / 8;
   p.v_first = (d.q_heads + d.k_heads) * d.head_dim / 8;
   if (v_heads) {
-    const long long rows = (long long)d.tokens * d.groups, want = 8ll * blocks;
-    const long long nb = (rows + kQkWarps - 1) / kQkWarps;
+    const long long rows = (long long)d.tokens * d.groups, want = 4ll * blocks;
+    const long long nb = (rows + 4 * kQkWarps - 1) / (4 * kQkWarps);
     p.v_blocks = (int)(nb < want ? nb : want);
   }
   p.x_ld = d.x_ld; p.x_gs = d.x_gstride; p.y_ld = d.y_ld; p.y_gs = d.y_gstride;
