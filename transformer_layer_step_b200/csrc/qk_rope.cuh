@@ -25,7 +25,9 @@ namespace gptl {
 
 constexpr int kQkWarps = 8;             // warps of a block
 constexpr int kQkMaxBlocks = 592;       // partial rows of the gains' gradients
-constexpr int kQkFwdBlocks = 4, kQkBwdBlocks = 2;              // resident on an SM
+// Blocks resident on an SM, by registers: the forward takes 64, the backward 80, or
+// 128 with the gains' gradients (at 80 that one spills: 49 -> 92 us).
+constexpr int qk_blocks(bool bwd, bool norm) { return !bwd ? 4 : norm ? 2 : 3; }
 constexpr double kQkAngles = 1.0;       // cost of a token's angles, in slots
 
 // The heads of one kind.  A slot is a warp's step: 32/lanes heads of a token, counted
@@ -200,7 +202,7 @@ __device__ void qk_copy_values(const QkParams &p, const T *from, long long f_ld,
 
 // BWD: out = dx from x and dy; else out = y from x.  NORM: with gains.
 template <typename T, int LANES, bool INTER, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kQkWarps * 32, BWD ? kQkBwdBlocks : kQkFwdBlocks)
+__global__ void __launch_bounds__(kQkWarps * 32, qk_blocks(BWD, NORM))
     qk_rope_kernel(const QkParams p) {
   constexpr bool kX = NORM || !BWD;                        // x is read
   __shared__ __align__(16) float4 cs_all[kQkWarps][4 * 16];
@@ -627,7 +629,7 @@ int gptl_qk_norm_rope_fwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   int sms = 0;
   GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  QkParams p = qk_params(d, in_place ? 0 : d.v_heads, sms * kQkFwdBlocks);
+  QkParams p = qk_params(d, in_place ? 0 : d.v_heads, sms * qk_blocks(false, gq != nullptr));
   p.x = x;
   p.out = y;
   p.gain[0] = gq;
@@ -663,7 +665,7 @@ int gptl_qk_norm_rope_bwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   int sms = 0;
   GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  int most = sms * kQkBwdBlocks;
+  int most = sms * qk_blocks(true, gq != nullptr);
   if (most > kQkMaxBlocks) most = kQkMaxBlocks;
   QkParams p = qk_params(d, dy == dx ? 0 : d.v_heads, most);
   p.x = x;
