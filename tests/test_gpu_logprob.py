@@ -153,6 +153,19 @@ def test_fwd_bwd(dtype, rows, vocab, pad, top_k, kind):
     _check_bwd(d_t[:rows, :vocab].double().cpu().numpy(), x, None, zero, de, want, dtype)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 149])
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 511), ("bf16", 527), ("bf16", 4096), ("fp32", 4200), ("fp16", 8192),
+                                         ("fp32", 2051), ("bf16", 16390)])
+def test_between_the_splits(rows, dtype, vocab):
+    """Sizes at which the work goes over from a warp to a block, and to clusters."""
+    need_gpu()
+    x_t, x = _logits(rows, vocab, vocab + 1, dtype, rows)
+    t = np.arange(rows, dtype=np.int32)
+    o = _fwd(x_t, rows, vocab, vocab + 1, dtype, torch.from_numpy(t).cuda(), 0)
+    check_device_error()
+    _check_fwd(o, x, t, 0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("vocab", [37, 9003])
 def test_rows_that_masks_and_infinities_leave(dtype, vocab):

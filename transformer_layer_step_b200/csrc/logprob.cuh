@@ -41,9 +41,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kLpMaxWarps = 16;
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpFill = 1, kLpNarrow = 5;
-constexpr int kLpBwdVecs = 32, kLpBwdWarps = 64;
-constexpr int kLpWarpVecs = 256;        // longest row of a warp, in vectors
+constexpr int kLpNarrow = 5;            // blocks an SM from which on they are narrow
+constexpr int kLpWarpVecs = 64, kLpWarpVecsMany = 2048, kLpManyRows = 8;   // rows of a warp
+constexpr int kLpBwdVecs = 32, kLpBwdWarps = 64;   // gradient: a lane's vectors, warps of an SM
 constexpr int kLpBatch = 4;             // 16-byte loads of a thread in a batch
 constexpr int kLpShortBatch = 2;        // the same where a warp takes a short row
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
@@ -654,18 +654,30 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   p.top_k = top_k;
   p.top_logp = top_logp;
   p.top_id = top_id;
-  // A row's blocks: 1 once the rows fill the SMs, else up to 8 of at least
-  // 2048 elements each.
+  // Short rows go to a warp each: up to 64 vectors always (100 x 500 bf16: 2.4 us
+  // against a block's 2.7; 100 x 2000: 3.1 against 2.8), up to 2048 once there are
+  // warps enough for every SM (8192 x 4000: 19 against 33; 8192 x 16000: 55 against
+  // 58; 600 x 2000: 3.7 against
+  // 3.4).  The alternatives need a block's shared memory.
+  const int vecs = vocab / (logits_f32 ? 4 : 8);
+  const bool warp_rows =
+      top_k == 0 && (vecs <= kLpWarpVecs || (vecs <= kLpWarpVecsMany && rows >= kLpManyRows * sms));
+  // Else a row's blocks: 1 once the rows fill the SMs, up to 8 of at least 2048
+  // elements each before (64 x 128000: 4 blocks 6.9 us, 8 blocks 7.7; going on to
+  // 8 blocks an SM, 1000 x 32000 fp32 takes 29 us instead of 26).
   int cs = 1;
-  while (cs < kLpMaxCluster && (long long)rows * cs < (long long)kLpFill * sms && vocab / (2 * cs) >= 2048) {
+  while (!warp_rows && cs < kLpMaxCluster && (long long)rows * cs < sms && vocab / (2 * cs) >= 2048) {
     cs *= 2;
     ++p.cluster_log2;
   }
-  const int vecs = vocab / (logits_f32 ? 4 : 8) / cs;
-  const bool warp_rows = top_k == 0 && (vecs <= kLpWarpVecs || (vecs <= 4 * kLpWarpVecs && rows >= 8 * sms));
-  const int threads = !warp_rows && vecs >= 256 && (long long)rows * cs < (long long)kLpNarrow * sms ? 256 : 128;
-  if ((long long)rows * cs >= (1ll << 31)) return GPTL_E_SHAPE;
-  const unsigned grid = warp_rows ? (unsigned)((rows + 3ll) / 4) : (unsigned)rows * (unsigned)cs;
+  // 256 threads a block while blocks are few (300 x 128000: 25 us, with 128 35), 128
+  // once they fill the SMs, which wait less at the end of a row (8192 x 50257: 156
+  // and 147 us before the loads were overlapped, 1000 x 32000 fp32 with 5
+  // alternatives 33 and 30).
+  const long long blocks = (long long)rows * cs;
+  const int threads = !warp_rows && vecs / cs >= 256 && blocks < kLpNarrow * sms ? 256 : 128;
+  if (blocks >= (1ll << 31)) return GPTL_E_SHAPE;
+  const unsigned grid = warp_rows ? (unsigned)((rows + 3ll) / 4) : (unsigned)blocks;
   prof_start(st);
   if (logits_f32) GPTL_TRY(launch_lp_fwd<float>(p, warp_rows, grid, threads, st));
   else if (dtype == GPTL_FP16) GPTL_TRY(launch_lp_fwd<__half>(p, warp_rows, grid, threads, st));
@@ -697,8 +709,9 @@ int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   p.dentropy = dentropy;
   p.dlogits = dlogits;
   // A warp's part of a row: as long as leaves kLpBwdWarps warps an SM, so that the
-  // row's scalars and the first loads are small beside it, but at most kLpBwdVecs
-  // vectors a lane, and one batch at least.
+  // row's scalars and the first loads are small beside it (4096 x 50257 with one
+  // batch a thread 168 us, with 32 vectors 137), but at most kLpBwdVecs vectors a
+  // lane, and one batch at least.
   const int vecs = vocab / (logits_f32 ? 4 : 8) + 1;
   long long lane_vecs = (long long)rows * vecs / (32ll * kLpBwdWarps * sms);
   if (lane_vecs > kLpBwdVecs) lane_vecs = kLpBwdVecs;

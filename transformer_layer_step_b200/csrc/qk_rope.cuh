@@ -643,7 +643,7 @@ int gptl_qk_norm_rope_fwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
 size_t gptl_qk_norm_rope_scratch_bytes(const gptl_qk_desc *desc) {
   gptl_qk_desc d;
   if (!desc || check_qk(*desc, GPTL_BF16, &d) != GPTL_OK) return 0;
-  return (size_t)2 * kQkMaxBlocks * (size_t)d.head_dim * sizeof(float);
+  return (size_t)kQkMaxBlocks * (size_t)d.head_dim * sizeof(float);
 }
 
 int gptl_qk_norm_rope_bwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void *x, const void *dy,
