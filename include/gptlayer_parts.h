@@ -263,7 +263,7 @@ size_t gptl_qk_norm_rope_scratch_bytes(const gptl_qk_desc *d);
  * and dx have the y strides; dx is dy itself (V columns are left alone) or
  * overlaps neither dy nor x (V columns are copied).  dgq, dgk: fp32
  * [head_dim], overwritten with the sums over all tokens, groups and heads, in
- * a fixed order; given exactly when gq and gk are, as is scratch. */
+ * a fixed order; given exactly when gq and gk are, and scratch with them. */
 int gptl_qk_norm_rope_bwd(const gptl_qk_desc *d, gptl_dtype dtype, const void *x, const void *dy,
                           void *dx, const void *gq, const void *gk, const int *pos,
                           const gptl_rope_pair *table, float *dgq, float *dgk, void *scratch,
@@ -295,8 +295,8 @@ int gptl_rng_advance(gptl_rng_state *rng, unsigned long long n, gptl_stream_t st
  * resid_f32, else cdt) may be NULL; y is fp32 when y_f32, else cdt.  The sum is
  * fp32, rounded once.  y may be x or resid itself where their types agree, and
  * overlaps no input otherwise.  h % 8 == 0, rows*h < 2^35 (GPTL_E_SHAPE);
- * 0 <= p and floor(p * 65536 + 1/2) < 65536 (GPTL_E_ARG); p = 0 reads no
- * state.  rng may be NULL only for p = 0. */
+ * 0 <= p and D < 65536 (GPTL_E_ARG); with D = 0 (p < 2^-17) nothing is dropped,
+ * and rng is not read and may be NULL. */
 int gptl_dropout_add_fwd(int rows, int h, gptl_dtype dtype, const void *x, const void *bias,
                          const void *resid, int resid_f32, float p, const gptl_rng_state *rng,
                          unsigned site, void *y, int y_f32, gptl_stream_t stream);
@@ -306,7 +306,8 @@ size_t gptl_dropout_scratch_bytes(int rows, int h);
 
 /* dx (cdt) = dy where kept, times the forward's factor, else 0; dbias (fp32
  * [h], may be NULL, else scratch is needed) = the column sums of that product
- * before it is rounded to dx, in a fixed order.  dy is fp32 when dy_f32, else
+ * before it is rounded to dx, in a fixed order; calls that share scratch must be
+ * ordered on the device.  dy is fp32 when dy_f32, else
  * cdt; dx may be dy itself where the types agree.  The gradient of resid is dy.
  * Other arguments and errors as the forward's. */
 int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int dy_f32, float p,
@@ -332,7 +333,8 @@ int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int 
  * rows >= 1 (GPTL_E_SHAPE).
  * x_v = -inf has probability 0.  A row of nothing else gives m = ln Z = -inf,
  * entropy 0, logp and top_logp -inf, top_id 0, 1, ...  A row with +inf or NaN
- * gives NaN in every output (m: +inf or NaN's row maximum) and top_id -1. */
+ * gives NaN in every output (m: the largest element that is not NaN) and
+ * top_id -1. */
 int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, int logits_f32,
                            const void *logits, const int *target, float *logp, float *entropy,
                            float *stats, int top_k, float *top_logp, int *top_id,

@@ -15,6 +15,13 @@
 // down the rows, so the bias is read once and the bias gradient is summed in
 // registers, in the order of the rows.
 //
+// B200, GPU time (share of the bytes at 6535 GB/s): forward 2048 x 10240 with a 32-bit
+// residual 33 us (0.97), 8192 x 2560 fp16 26.5 (0.73); backward 8192 x 2560 fp16 18.0 us
+// (0.71), with the bias gradient 21.5 (0.60: the second kernel and the first one's
+// end), 2048 x 10240 from 32 bits with it 24.6 (0.78); 128 x 128 2.4 us, a launch's
+// time.  Two rows in flight a thread at four blocks an SM: with four rows the
+// backward spills (22.7 us), with six blocks too (26.4).
+//
 // Included by libgptlayer.cu after gptlayer.cu, in the same translation unit.
 #pragma once
 
