@@ -209,9 +209,10 @@ def strerror(code: int) -> str:
 def _ptr(x) -> int | None:
     if x is None:
         return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return x
-    return x.data_ptr()
 
 
 def _check(rc: int, where: str):
