@@ -203,8 +203,9 @@ int gptl_colsum_noalloc(int rows, int n, int groups, long long ld, long long gst
  *     phi = 2 pi * pos[axis_j][token] * turns_j
  *     y_a = n_a cos(phi) - n_b sin(phi),   y_b = n_b cos(phi) + n_a sin(phi)
  *   the other elements of y are those of n.
- * Statistics and rotation are fp32, the angle's turns are reduced in fp64
- * (exact to fp32 for every int position), and y is rounded once.
+ * Statistics and rotation are fp32, the angle's turns are reduced in fixed point
+ * (exact to fp32 for every int position), and y is rounded once.  (A bf16 head whose
+ * squares leave fp32, beyond 1e18, comes out as 0.)
  * interleaved = 0 pairs elements (j, j + rot_dim/2), 1 pairs (2j, 2j + 1). */
 typedef struct {
   int tokens, groups;              /* rows of a group, groups (tp shards);    */

@@ -215,6 +215,20 @@ def test_zero_and_infinite_heads():
     assert same.all()
 
 
+@pytest.mark.parametrize("eps,scale", [(1e-30, 1.5), (1e-30, 1e-12), (1e-5, 1e15), (1e30, 1.5)])
+def test_far_scales(eps, scale):
+    """r from 1e-15 to 1e15, whose cube is outside fp32, and a head of zeros."""
+    c = Case("bf16", 5, 1, 2, 1, 0, 64, 64, 0, 1, 100, scale=scale)
+    c.x[0, 2] = 0.0
+    c.eps = c.desc.eps = float(np.float32(eps))
+    x_t, y_t, dx_t = c.buffer(c.x), c.buffer(None), c.buffer(None)
+    c.fwd(x_t, y_t)
+    dg = c.bwd(x_t, c.buffer(c.dy), dx_t)
+    check_device_error()
+    c.check_fwd(y_t)
+    c.check_bwd(dx_t, dg)
+
+
 def test_bad_axis_is_reported():
     """An axis outside the descriptor's sets bit 2 of the error word and counts
     as axis 0; the table is read within its bounds all the same."""

@@ -20,6 +20,13 @@ def _code(fn, *args, **kw):
     return e.value.code
 
 
+def test_launch_kinds_have_names():
+    import os
+    import re
+    text = open(os.path.join(G.INCLUDE, "gptlayer_profile.h")).read()
+    assert int(re.search(r"GPTL_KIND_COUNT = (\d+)", text).group(1)) == len(G.KIND_NAMES)
+
+
 # ------------------------------------------------------ queries and keys
 def _qk(**kw):
     return G.make_qk_desc(**{**dict(tokens=4, groups=2, q_heads=4, k_heads=2, v_heads=2, head_dim=64,

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, qk_blocks(BWD, NORM))
           sd = d2.x + d2.y;
           qk_head_sum<LANES, true>(p, lane, c, ss, sd);
           const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-          const float m = -r * r * r * (sd * p.inv_hd);
+          const float m = -(sd * p.inv_hd * r) * r * r;    // r^3 alone may leave fp32
           const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
