@@ -330,8 +330,8 @@ int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int 
  * means none (logp = 0); one >= vocab sets bit 2 of the device error word and
  * gives logp = NaN.  target and logp come together or not at all; entropy,
  * stats and the top pair (with top_k = 0) are optional, but one output is
- * given.  0 <= top_k <= 32 and <= vocab (GPTL_E_ARG); 1 <= vocab < 2^30,
- * rows >= 1 (GPTL_E_SHAPE).
+ * given.  0 <= top_k <= 32 and <= vocab (GPTL_E_ARG); 1 <= vocab < 2^30, with
+ * alternatives <= 2^20, rows >= 1 (GPTL_E_SHAPE).
  * x_v = -inf has probability 0.  A row of nothing else gives m = ln Z = -inf,
  * entropy 0, logp and top_logp -inf, top_id 0, 1, ...  A row with +inf or NaN
  * gives NaN in every output (m: the largest element that is not NaN) and

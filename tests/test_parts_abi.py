@@ -140,6 +140,7 @@ def test_logprob_arguments_refused():
     assert fwd(k=3) == G.E_NULL and fwd(k=3, tv=A) == G.E_NULL
     for kw in (dict(k=-1), dict(k=33), dict(k=8, vocab=7)):
         assert fwd(**kw, tv=A, ti=A) == G.E_ARG, kw
+    assert fwd(k=1, vocab=(1 << 20) + 1, ld=1 << 21, tv=A, ti=A) == G.E_SHAPE
     assert fwd(x=A + 2) == G.E_ALIGN and fwd(target=A + 2) == G.E_ALIGN and fwd(ent=A + 1) == G.E_ALIGN
 
     def bwd(rows=2, vocab=100, ld=100, x=A, target=A, stats=A, ent=A, up=A, de=A, dx=FAR):

@@ -10,8 +10,9 @@
 // The forward reads the logits once: each thread keeps a running maximum and
 // rescales its Z and S when it grows, once for 64 bytes at most.  x - m is formed
 // before it is scaled, so that neither a mask of the type's lowest value nor
-// large logits lose the difference.  Sums are fp32, each of at most a few
-// hundred terms before they are joined in a tree.
+// large logits lose the difference.  Sums are fp32, of vocab / 256 terms before they
+// are joined in a tree (a batch's own sums first, for longer rows: 2 % slower at
+// 8192 x 50257 and 5 % at the clocks of a long run).
 //
 // Bound by HBM (2 or 4 bytes an element forward, twice that backward), with
 // one exponential an element close behind (16 a clock and SM: 0.72 of the unit's
@@ -21,9 +22,9 @@
 // gradient a warp takes a part of a row.
 //
 // B200, GPU time (share of the bytes at 6535 GB/s): forward with entropy 8192 x 50257
-// bf16 135 us (0.93), 1000 x 32000 fp32 24.8 (0.79), with 5 alternatives 30.1 (0.65),
-// 2048 x 50257 bf16 41.5 (0.76), with 20 alternatives 63 (0.50), 8192 x 1000 7.7 (0.33),
-// 5 x 50257 4.3 us, with 20 alternatives 8.8; gradient 4096 x 50257 bf16 138 us (0.91),
+// bf16 136 us (0.93), 1000 x 32000 fp32 25.1 (0.78), with 5 alternatives 30 (0.65),
+// 2048 x 50257 bf16 43 (0.73), with 20 alternatives 65 (0.48), 8192 x 1000 7.7 (0.33),
+// 5 x 50257 4.4 us, with 20 alternatives 8.8; gradient 4096 x 50257 bf16 138 us (0.91),
 // 2048 x 50304 fp32 132 (0.96), 8192 x 1000 bf16 8.9 (0.57).
 //
 // Top alternatives: a thread remembers in which vector it saw its maximum.  The
@@ -48,7 +49,7 @@ namespace gptl {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpMaxWarps = 16;
+constexpr int kLpMaxWarps = 8;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpNarrow = 5;            // blocks an SM from which on they are narrow
 constexpr int kLpWarpVecs = 64, kLpWarpVecsMany = 2048, kLpManyRows = 8;   // rows of a warp
@@ -187,6 +188,9 @@ constexpr int kLpGroups = 64;           // groups of threads whose maxima bound 
 constexpr int kLpHits = 256;            // vectors that may hold candidates
 constexpr int kLpCandidates = 1024;     // more than a slice that leaves groups empty has
 
+constexpr int kLpPasses = 8192;
+constexpr int kLpMaxTopVocab = 1 << 20;
+
 struct LpTop {
   uint4 hit[kLpHits];
   unsigned long long group[kLpGroups], least;
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
   static_assert(!(TOP && WARP), "the alternatives take a block");
   constexpr int N = LpVec<T>::N;
   __shared__ LpSum warp_sum[kLpMaxWarps], rank_sum[kLpMaxCluster];
-  __shared__ float final_stats[3];                           // m, ln Z, 1 if the row is bad
+  __shared__ float final_stats[3];                           // m, ln Z, 1 for NaN, 2 for -inf alone
   __shared__ std::conditional_t<TOP, LpTop, int> top[1];
   __shared__ unsigned long long rank_top[TOP ? kLpMaxCluster * 32 : 1];
   cg::cluster_group cluster = cg::this_cluster();
@@ -339,9 +343,11 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
       p.stats[2 * row] = w.m;
       p.stats[2 * row + 1] = lz;
     }
-    final_stats[0] = w.m;
-    final_stats[1] = lz;
-    final_stats[2] = bad ? 1.f : empty ? 2.f : 0.f;
+    if constexpr (TOP) {
+      final_stats[0] = w.m;
+      final_stats[1] = lz;
+      final_stats[2] = bad ? 1.f : empty ? 2.f : 0.f;
+    }
   };
   if constexpr (WARP) {
     if (lane == 0) finish(t);
@@ -379,7 +385,7 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
       if (rank == p.top_k - 1) S.least = k;
     }
     __syncthreads();
-    while (true) {
+    for (int pass = 1;; ++pass) {
       const unsigned long long least = S.least;
       const float least_value = least ? lp_key_value(least) : -INFINITY;
       auto offer = [&](unsigned long long k) {
@@ -442,8 +448,13 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
       }
       __syncthreads();
       if (whole) break;
-      // more than were kept: the k-th of those kept is a sharper bound (of kLpHits
-      // vectors all but one hold a candidate, so there is a k-th)
+      // More than were kept: the k-th of those kept is a sharper bound (of kLpHits
+      // vectors all but one hold a candidate, so there is a k-th).  It leaves over 200
+      // fewer each time, so 2^20 elements end long before the limit.
+      if (pass == kLpPasses) {
+        if (tid == 0) set_device_error(kErrIndex);
+        break;
+      }
       if (mine) S.least = mine;
       if (tid == 0) S.found = S.hits = 0;
       __syncthreads();
@@ -655,6 +666,7 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   LpParams p{};
   GPTL_TRY(check_lp(rows, vocab, ld, dtype, logits_f32, logits, target, &p));
   if (top_k < 0 || top_k > 32 || top_k > vocab) return GPTL_E_ARG;
+  if (top_k && vocab > kLpMaxTopVocab) return GPTL_E_SHAPE;
   if (top_k && (!top_logp || !top_id)) return GPTL_E_NULL;
   if (!aligned4(logp) || !aligned4(entropy) || !aligned4(stats) || !aligned4(top_logp) ||
       !aligned4(top_id))
