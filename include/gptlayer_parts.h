@@ -210,7 +210,8 @@ int gptl_colsum_noalloc(int rows, int n, int groups, long long ld, long long gst
 typedef struct {
   int tokens, groups;              /* rows of a group, groups (tp shards);    */
                                    /* tokens * groups < 2^30                  */
-  int q_heads, k_heads, v_heads;   /* of one group; v_heads may be 0          */
+  int q_heads, k_heads, v_heads;   /* of one group; v_heads may be 0; their   */
+                                   /* sum times groups at most 2^20           */
   int head_dim;                    /* multiple of 16, at most 256             */
   int rot_dim;                     /* multiple of 16, 0 .. head_dim           */
   int interleaved;                 /* 0 or 1                                  */
