@@ -374,8 +374,11 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
     const unsigned long long g = key_max(low, width);
     if (tid % width == 0) S.group[tid / width] = g;
     if (tid == 0) S.found = S.hits = 0;
-    __syncthreads();
-    {
+    if (tid < 32) S.best[tid] = 0;
+    // A NaN or +inf in the block's part (their sum is NaN) leaves the row no
+    // alternatives, and an order of keys with NaN among them no k-th: no search.
+    const bool bad_part = __syncthreads_or(!(a.z < INFINITY));
+    if (!bad_part) {
       // (empty groups are all 0: the first of equals takes the place)
       const int mine = tid / width;
       const unsigned long long k = S.group[mine];
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
       if (rank == p.top_k - 1) S.least = k;
     }
     __syncthreads();
-    for (int pass = 1;; ++pass) {
+    for (int pass = 1; !bad_part; ++pass) {
       const unsigned long long least = S.least;
       const float least_value = least ? lp_key_value(least) : -INFINITY;
       auto offer = [&](unsigned long long k) {
@@ -492,15 +495,19 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
   if constexpr (TOP) {
     __syncthreads();
     const float kind = final_stats[2];
-    auto put = [&](int place, unsigned long long k) {
-      const float lp = kind == 1.f   ? __int_as_float(0x7FC00000)
-                       : kind == 2.f ? -INFINITY
-                                     : (lp_key_value(k) - final_stats[0]) - final_stats[1];
+    auto put = [&](int place, float lp, int id) {
       p.top_logp[row * p.top_k + place] = lp;
-      p.top_id[row * p.top_k + place] = kind == 1.f ? -1 : lp_key_index(k);
+      p.top_id[row * p.top_k + place] = id;
+    };
+    if (kind == 1.f) {                                       // a bad part left no keys to rank
+      if (tid < p.top_k) put(tid, __int_as_float(0x7FC00000), -1);
+      return;
+    }
+    auto put_key = [&](int place, unsigned long long k) {
+      put(place, kind == 2.f ? -INFINITY : (lp_key_value(k) - final_stats[0]) - final_stats[1], lp_key_index(k));
     };
     if (cs == 1) {
-      if (tid < p.top_k) put(tid, top[0].best[tid]);
+      if (tid < p.top_k) put_key(tid, top[0].best[tid]);
     } else {
       for (int i = tid; i < cs * p.top_k; i += nt) {
         const unsigned long long k = rank_top[i];
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
 #pragma unroll
         for (int r = 0; r < kLpMaxCluster; ++r)
           if (r < cs) place += key_rank_sorted(k, rank_top + r * p.top_k, p.top_k);
-        if (place < p.top_k) put(place, k);
+        if (place < p.top_k) put_key(place, k);
       }
     }
   }
