@@ -209,10 +209,9 @@ def strerror(code: int) -> str:
 def _ptr(x) -> int | None:
     if x is None:
         return None
-    try:
-        return x.data_ptr()
-    except AttributeError:
+    if isinstance(x, int):
         return x
+    return x.data_ptr()                  # a host array has none: refused here
 
 
 def _check(rc: int, where: str):
