@@ -246,7 +246,9 @@ int gptl_rope_table(int rot_dim, int axes, const int *axis_pairs, int per_axis, 
 /* Forward: x -> y.  y is x itself (same strides: in place; V columns are left
  * alone) or does not overlap it (V columns are copied, so that y is the whole
  * buffer that attention reads; training keeps x for the backward).  Columns
- * between the row width and ld are not touched.
+ * between the row width and ld are not touched; y may lie in those of x, or x
+ * in those of y, where the two have the same strides (with other strides the
+ * whole ranges, first to last element, have to be apart).
  * gq, gk: [head_dim] (cdt), both or neither.  pos: int32 [axes][tokens] or
  * NULL.  table: [rot_dim/2], may be NULL when rot_dim is 0; an axis outside
  * [0, axes) sets bit 2 of the device error word and counts as axis 0.
@@ -263,7 +265,7 @@ size_t gptl_qk_norm_rope_scratch_bytes(const gptl_qk_desc *d);
 
 /* Backward: dx from the forward's x (x strides) and dy, the gradient of y.  dy
  * and dx have the y strides; dx is dy itself (V columns are left alone) or
- * overlaps neither dy nor x (V columns are copied).  dgq, dgk: fp32
+ * overlaps neither dy nor x, in the sense above (V columns are copied).  dgq, dgk: fp32
  * [head_dim], overwritten with the sums over all tokens, groups and heads, in
  * a fixed order; given exactly when gq and gk are, and scratch with them. */
 int gptl_qk_norm_rope_bwd(const gptl_qk_desc *d, gptl_dtype dtype, const void *x, const void *dy,
@@ -342,7 +344,8 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
                            float *stats, int top_k, float *top_logp, int *top_id,
                            gptl_stream_t stream);
 
-/* dlogits (type and ld of logits; may be logits itself, else no overlap), for
+/* dlogits (type and ld of logits; logits itself, or no row of it overlaps one of
+ * logits: the columns from vocab to ld of one may hold the other), for
  * the upstream gradients dlogp and dentropy ([rows] fp32, either may be NULL,
  * not both):
  *   dx_v = dlogp (1[v = target] - p_v) - dentropy p_v (ln p_v + entropy)

@@ -730,8 +730,9 @@ int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
   if (!aligned16(dlogits) || !aligned4(stats) || !aligned4(entropy) || !aligned4(dlogp) ||
       !aligned4(dentropy))
     return GPTL_E_ALIGN;
-  const long long bytes = ((rows - 1) * ld + vocab) * (logits_f32 ? 4 : 2);
-  if (dlogits != logits && ranges_overlap(logits, bytes, dlogits, bytes)) return GPTL_E_ARG;
+  const long long es = logits_f32 ? 4 : 2;
+  if (dlogits != logits && rows_overlap(logits, dlogits, RowsShape{1, 0, rows, es * ld, es * vocab}))
+    return GPTL_E_ARG;
   int sms = 0;
   GPTL_TRY(device_check(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

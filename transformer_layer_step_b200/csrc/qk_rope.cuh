@@ -30,6 +30,8 @@
 // Included by libgptlayer.cu after gptlayer.cu, in the same translation unit.
 #pragma once
 
+#include <utility>
+
 #include "gptlayer_parts.h"
 
 namespace gptl {
@@ -487,14 +489,50 @@ int check_qk(const gptl_qk_desc &d, gptl_dtype dt, gptl_qk_desc *out) {
   return GPTL_OK;
 }
 
-long long qk_span_bytes(const gptl_qk_desc &d, long long ld, long long gs) {
-  const long long width = ((long long)d.q_heads + d.k_heads + d.v_heads) * d.head_dim;
-  return 2 * ((d.groups - 1) * gs + (long long)(d.tokens - 1) * ld + width);
-}
-
 bool ranges_overlap(const void *a, long long na, const void *b, long long nb) {
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
   return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
+// The same for two sets of rows with the same strides, `shape` = {groups, gstride,
+// tokens, ld, width} in bytes: only the rows count, not what lies between them, so
+// that column ranges of one buffer are apart.  (rows of a set never overlap; at most
+// 2^15 steps, tokens * groups being below 2^30)
+struct RowsShape {
+  long long groups, gstride, tokens, ld, width;
+  long long span() const { return (groups - 1) * gstride + (tokens - 1) * ld + width; }
+};
+bool rows_overlap(const void *a, const void *b, RowsShape s) {
+  if (!ranges_overlap(a, s.span(), b, s.span())) return false;
+  if (s.tokens < s.groups) {
+    std::swap(s.tokens, s.groups);
+    std::swap(s.ld, s.gstride);
+  }
+  const long long apart =
+      (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  for (long long g = 1 - s.groups; g < s.groups; ++g) {
+    const long long rest = apart - g * s.gstride;
+    long long t = s.tokens > 1 ? rest / s.ld - 1 : 0;          // ld >= width: three rows at most
+    const long long last = s.tokens > 1 ? t + 2 : 0;
+    for (; t <= last; ++t) {
+      const long long off = s.tokens > 1 ? rest - t * s.ld : rest;
+      if (t > -s.tokens && t < s.tokens && off < s.width && off > -s.width) return true;
+    }
+  }
+  return false;
+}
+
+RowsShape qk_rows(const gptl_qk_desc &d, long long ld, long long gs) {
+  const long long width = ((long long)d.q_heads + d.k_heads + d.v_heads) * d.head_dim;
+  return RowsShape{d.groups, 2 * gs, d.tokens, 2 * ld, 2 * width};
+}
+
+// x (x strides) and a buffer with the y strides: row by row where the strides agree.
+bool qk_overlap(const gptl_qk_desc &d, const void *x, const void *y) {
+  const RowsShape sx = qk_rows(d, d.x_ld, d.x_gstride), sy = qk_rows(d, d.y_ld, d.y_gstride);
+  if ((d.tokens == 1 || sx.ld == sy.ld) && (d.groups == 1 || sx.gstride == sy.gstride))
+    return rows_overlap(x, y, sx);
+  return ranges_overlap(x, sx.span(), y, sy.span());
 }
 
 // Lanes of a head: one for each 16 elements where that lets a warp hold more heads
@@ -633,8 +671,7 @@ int gptl_qk_norm_rope_fwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   const bool in_place = x == y;
   if (in_place) {
     if (d.x_ld != d.y_ld || d.x_gstride != d.y_gstride) return GPTL_E_ARG;
-  } else if (ranges_overlap(x, qk_span_bytes(d, d.x_ld, d.x_gstride), y,
-                            qk_span_bytes(d, d.y_ld, d.y_gstride))) {
+  } else if (qk_overlap(d, x, y)) {
     return GPTL_E_ARG;
   }
   int sms = 0;
@@ -669,9 +706,7 @@ int gptl_qk_norm_rope_bwd(const gptl_qk_desc *desc, gptl_dtype dtype, const void
   if (gq && (!dgq || !dgk || !scratch)) return GPTL_E_NULL;
   if (!gq && (dgq || dgk)) return GPTL_E_NULL;
   if (!aligned16(dgq) || !aligned16(dgk) || !aligned16(scratch)) return GPTL_E_ALIGN;
-  const long long xb = qk_span_bytes(d, d.x_ld, d.x_gstride);
-  const long long yb = qk_span_bytes(d, d.y_ld, d.y_gstride);
-  if (ranges_overlap(x, xb, dx, yb) || (dy != dx && ranges_overlap(dy, yb, dx, yb)))
+  if (qk_overlap(d, x, dx) || (dy != dx && rows_overlap(dy, dx, qk_rows(d, d.y_ld, d.y_gstride))))
     return GPTL_E_ARG;
   int sms = 0;
   GPTL_TRY(device_check(&sms));
