@@ -247,9 +247,13 @@ int drop_splits(int rows, int h, bool sums) {
   return (int)(most > 65535 ? 65535 : most);
 }
 
+bool drop_sizes(int rows, int h) {
+  return rows > 0 && h > 0 && h % 8 == 0 && (long long)rows * h < (1ll << 35);
+}
+
 int check_drop(int rows, int h, gptl_dtype dt, float p, const gptl_rng_state *rng, DropParams *a) {
   if (dt != GPTL_FP16 && dt != GPTL_BF16) return GPTL_E_DTYPE;
-  if (rows <= 0 || h <= 0 || h % 8 || (long long)rows * h >= (1ll << 35)) return GPTL_E_SHAPE;
+  if (!drop_sizes(rows, h)) return GPTL_E_SHAPE;
   if (!(p >= 0.f && p < 1.f)) return GPTL_E_ARG;
   const int d = (int)floor((double)p * 65536.0 + 0.5);
   if (d >= 65536) return GPTL_E_ARG;
@@ -318,7 +322,7 @@ int gptl_dropout_add_fwd(int rows, int h, gptl_dtype dtype, const void *x, const
 }
 
 size_t gptl_dropout_scratch_bytes(int rows, int h) {
-  if (rows <= 0 || h <= 0 || h % 8) return 0;
+  if (!drop_sizes(rows, h)) return 0;
   return (size_t)drop_splits(rows, h, true) * (size_t)h * sizeof(float);
 }
 
