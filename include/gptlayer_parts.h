@@ -220,7 +220,8 @@ typedef struct {
   float eps;                       /* > 0 when there are gains                */
   /* element (group, token, c) of x is at x + group*x_gstride + token*x_ld + c,
    * of y at y + group*y_gstride + token*y_ld + c: multiples of 8, 0 for dense
-   * (ld = row width, gstride = tokens*ld) */
+   * (ld = row width, gstride = tokens*ld); each below 2^40, and tokens*ld and
+   * groups*gstride below 2^56 */
   long long x_ld, x_gstride, y_ld, y_gstride;
 } gptl_qk_desc;
 
@@ -322,7 +323,7 @@ int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int 
  * Log probabilities of given tokens under softmax(logits), with the entropy
  * and the top alternatives, in one pass over the logits.
  *   logits: [rows] of vocab elements, ld elements apart (ld >= vocab, any
- *           value), fp32 when logits_f32, else cdt
+ *           value below 2^40, rows*ld below 2^56), fp32 when logits_f32, else cdt
  *   m = max_v x_v,  Z = sum_v exp(x_v - m)
  *   logp    = x_target - m - ln Z
  *   entropy = ln Z - sum_v p_v (x_v - m),   p_v = exp(x_v - m) / Z

@@ -624,7 +624,8 @@ int check_lp(int rows, int vocab, long long ld, gptl_dtype dt, int f32, const vo
              const int *target, LpParams *p) {
   if (dt != GPTL_FP16 && dt != GPTL_BF16) return GPTL_E_DTYPE;
   if (f32 != 0 && f32 != 1) return GPTL_E_ARG;
-  if (rows < 1 || vocab < 1 || vocab >= (1 << 30) || ld < vocab || ld >= (1ll << 40))
+  if (rows < 1 || vocab < 1 || vocab >= (1 << 30) || ld < vocab || ld >= (1ll << 40) ||
+      !far_rows(rows, ld))
     return GPTL_E_SHAPE;
   if (!aligned16(logits) || (reinterpret_cast<uintptr_t>(target) & 3u)) return GPTL_E_ALIGN;
   p->logits = logits;

@@ -459,6 +459,11 @@ int launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t st, A..
   return GPTL_OK;
 }
 
+// rows * ld, or 0 where that is 2^56 or more (rows >= 1, ld < 2^56).
+long long far_rows(long long rows, long long ld) {
+  return rows < (1ll << 56) / ld ? rows * ld : 0;
+}
+
 // Sizes and strides of a descriptor; dense strides filled in.
 int check_qk(const gptl_qk_desc &d, gptl_dtype dt, gptl_qk_desc *out) {
   if (dt != GPTL_FP16 && dt != GPTL_BF16) return GPTL_E_DTYPE;
@@ -478,7 +483,11 @@ int check_qk(const gptl_qk_desc &d, gptl_dtype dt, gptl_qk_desc *out) {
     if (ld < 0 || gs < 0 || ld % 8 || gs % 8 || ld >= (1ll << 40) || gs >= (1ll << 40))
       return GPTL_E_SHAPE;
     if (ld == 0) ld = width;
-    if (gs == 0) gs = (long long)d.tokens * ld;
+    // offsets stay below 2^56 elements, more than there are addresses for
+    const long long column = far_rows(d.tokens, ld);
+    if (!column) return GPTL_E_SHAPE;
+    if (gs == 0) gs = column;
+    if (!far_rows(d.groups, gs)) return GPTL_E_SHAPE;
     if (d.tokens > 1 && ld < width) return GPTL_E_SHAPE;
     if (d.groups > 1 && gs < width) return GPTL_E_SHAPE;
     // groups outside tokens, or tokens outside groups: rows never overlap
