@@ -204,8 +204,9 @@ int gptl_colsum_noalloc(int rows, int n, int groups, long long ld, long long gst
  *     y_a = n_a cos(phi) - n_b sin(phi),   y_b = n_b cos(phi) + n_a sin(phi)
  *   the other elements of y are those of n.
  * Statistics and rotation are fp32, the angle's turns are reduced in fixed point
- * (exact to fp32 for every int position), and y is rounded once.  (A bf16 head whose
- * squares leave fp32, beyond 1e18, comes out as 0.)
+ * (exact to fp32 for every int position where turns < 1/4, as of every base >= 1),
+ * and y is rounded once.  (A bf16 head whose squares leave fp32, beyond
+ * 1e18, comes out as 0, and so do its gradients where their products stay in fp32.)
  * interleaved = 0 pairs elements (j, j + rot_dim/2), 1 pairs (2j, 2j + 1). */
 typedef struct {
   int tokens, groups;              /* rows of a group, groups (tp shards);    */
@@ -268,7 +269,11 @@ size_t gptl_qk_norm_rope_scratch_bytes(const gptl_qk_desc *d);
  * and dx have the y strides; dx is dy itself (V columns are left alone) or
  * overlaps neither dy nor x, in the sense above (V columns are copied).  dgq, dgk: fp32
  * [head_dim], overwritten with the sums over all tokens, groups and heads, in
- * a fixed order; given exactly when gq and gk are, and scratch with them. */
+ * a fixed order; given exactly when gq and gk are, and scratch with them.
+ * Without gains the kernel does not read x, which has to be a valid address all
+ * the same (after a forward in place, that of y will do).  Calls that share
+ * scratch, those of two captured graphs among them, must be ordered on the
+ * device: each writes all the sums that it reads. */
 int gptl_qk_norm_rope_bwd(const gptl_qk_desc *d, gptl_dtype dtype, const void *x, const void *dy,
                           void *dx, const void *gq, const void *gk, const int *pos,
                           const gptl_rope_pair *table, float *dgq, float *dgk, void *scratch,
@@ -311,8 +316,8 @@ size_t gptl_dropout_scratch_bytes(int rows, int h);
 
 /* dx (cdt) = dy where kept, times the forward's factor, else 0; dbias (fp32
  * [h], may be NULL, else scratch is needed) = the column sums of that product
- * before it is rounded to dx, in a fixed order; calls that share scratch must be
- * ordered on the device.  dy is fp32 when dy_f32, else
+ * before it is rounded to dx, in a fixed order; calls that share scratch (those of
+ * two captured graphs among them) must be ordered on the device.  dy is fp32 when dy_f32, else
  * cdt; dx may be dy itself where the types agree.  The gradient of resid is dy.
  * Other arguments and errors as the forward's. */
 int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int dy_f32, float p,
@@ -338,8 +343,8 @@ int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int 
  * alternatives <= 2^20, rows >= 1 (GPTL_E_SHAPE).
  * x_v = -inf has probability 0.  A row of nothing else gives m = ln Z = -inf,
  * entropy 0, logp and top_logp -inf, top_id 0, 1, ...  A row with +inf or NaN
- * gives NaN in every output (m: the largest element that is not NaN) and
- * top_id -1. */
+ * gives NaN in every output (m: the largest element that is not NaN; logp of a
+ * negative target stays 0) and top_id -1 in every place. */
 int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, int logits_f32,
                            const void *logits, const int *target, float *logp, float *entropy,
                            float *stats, int top_k, float *top_logp, int *top_id,
@@ -355,7 +360,8 @@ int gptl_token_logprob_fwd(int rows, int vocab, long long ld, gptl_dtype dtype, 
  * of the device error word) takes dlogp = 0.  A row whose two gradients are
  * both 0 gets exact zeros whatever its logits; a row of -inf alone gets zeros; a
  * row with +inf or NaN gets NaN.  Columns from vocab to ld are not
- * touched. */
+ * touched: a product that runs over the padded width needs zeros there, and in
+ * place they still hold the padded logits. */
 int gptl_token_logprob_bwd(int rows, int vocab, long long ld, gptl_dtype dtype, int logits_f32,
                            const void *logits, const int *target, const float *stats,
                            const float *entropy, const float *dlogp, const float *dentropy,

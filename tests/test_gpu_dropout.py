@@ -5,8 +5,8 @@ Tolerances: z = x + bias, its product with the factor and the sum with resid are
 each rounded to fp32 (3 f of the absolute terms, f = 2^-24), and the result once
 to its type (u of its size; fp16 below its normal range 2^-25).  The mask is
 exact: every dropped element is resid to the last bit.  dbias sums at most
-rows / 8 terms in a thread and 8 * 148 partial rows after that: (rows + 1200) f
-of the sum of the absolute terms.
+rows / 8 terms in a thread, 256 teams of a block and 4 * 148 partial rows after that:
+under (rows + 1200) f of the sum of the absolute terms.
 """
 import numpy as np
 import pytest

@@ -6,7 +6,9 @@ twice and ex2.approx is good to 2^-22, so a term is off by 4 f + 3 f |t| of itse
 p-weighted, |t| is at most log2(vocab) + 2 in a row's mean.  A sum of positive terms
 is off by at most one f for each addition in its longest chain: with 128 threads and
 pairs of sums vocab / 256, and 16 in the trees and the remainder.  Z is good to
-R = f (4 + 3 (log2 vocab + 2) + vocab / 256 + 16) of itself.
+R = f (4 + 3 (log2 vocab + 2) + vocab / 256 + 16) of itself.  (Not counted: the factor
+of a maximum that grows, and the longer chains of a warp's row, vocab / 64 beyond 512
+elements in 1200 rows here; test_gpu_logprob_many_rows.py counts both.)
 * logp, top_logp: R + 3 f (|x - m| + ln Z).
 * entropy: R on ln Z, and on S / Z = sum p t twice R of sum p |t|, which is at
   most entropy + ln Z + 1: R (1 + 3 (ln Z + entropy + 1)).

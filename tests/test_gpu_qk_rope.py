@@ -3,14 +3,20 @@ backward, against the float64 oracle on the same 16-bit inputs.
 
 Tolerances, with u the 16-bit type's half step (2^-8, 2^-11) and f = 2^-24:
 * y = n_a cos - n_b sin is rounded once (u |y|) after fp32 arithmetic on terms
-  of at most N = max |n| of its head: r (two roundings of a sum of at most 256
-  squares in a tree of depth 16 + 4, and rsqrt: under 16 f), the gain, the
-  angle (f of its turns and of sincospi: under 6 f) and the products: 32 f N.
+  of at most N = max |n| of its head.  Each of these at its worst, with |a cos| +
+  |b sin| <= 1.42 N: the fast cosine and sine, 2^-21.19 and 2^-21.41 absolute as
+  documented, 7 f N and 6 f N; the angle's three roundings (its fixed-point turns to
+  fp32, the constant 2 pi / 2^32, their product), pi f each, 13.4 f N; the products'
+  roundings 2.4 f N: 29 f N for a rotation alone.  With gains, r (a chain of 14
+  additions of squares halved by the root, mean and eps 1, rsqrtf's 2 ulp: 12 f), x r
+  and the gain, 14 f of each term: 20 f N more.  The bar is 32 f N in both: above the
+  rotation's worst, and for the norm 0.65 of the sum of all worsts, which do not
+  meet in one element.
 * dx likewise, on terms of at most D = r max|d| + r^3 |x| mean|d x|, whose mean
   has a relative error of 24 f in its absolute sum: 64 f D.
 * dg sums dn x r over rows in fp32: at most 1024 additions in a lane's chain at
   these sizes, then 64 in trees: 1100 f of the sum of the absolute terms.  Each
-  dn is itself a rotation, off by 32 f of the head's largest |dy| as y is of N
+  dn is itself a rotation, off by 29 f of the head's largest |dy| as y is of N
   (not of |dn|, which may cancel): 32 f of the sum of max |dy| |x| r besides.
 * fp16 results below its normal range are rounded to multiples of 2^-24:
   2^-25 absolute.

@@ -10,17 +10,21 @@
 // 16-byte vector.  (32 bits an element would take two calls a vector, and the
 // integer multiplies would bound the backward, which moves 4 bytes an element.)
 //
-// Bound by HBM: 6 to 10 bytes an element forward, 4 to 6 backward.  A warp
+// Bytes: 4 to 10 an element forward, 4 to 6 backward.  A 32-bit residual stream is
+// bound by HBM.  16-bit streams are held up by the generator: a warp's vector takes
+// about 200 instructions forward and 140 backward, over half of the issue slots, and a
+// thread's next rows are loaded only after the present ones are stored.  A warp
 // reads 512 contiguous bytes of a row; a thread keeps its 8 columns and walks
 // down the rows, so the bias is read once and the bias gradient is summed in
 // registers, in the order of the rows.
 //
 // B200, GPU time (share of the bytes at 6535 GB/s): forward 2048 x 10240 with a 32-bit
-// residual 33 us (0.97), 8192 x 2560 fp16 26.5 (0.73); backward 8192 x 2560 fp16 18.0 us
-// (0.71), with the bias gradient 21.5 (0.60: the second kernel and the first one's
-// end), 2048 x 10240 from 32 bits with it 24.6 (0.78); 128 x 128 2.4 us, a launch's
-// time.  Two rows in flight a thread at four blocks an SM: with four rows the
-// backward spills (22.7 us), with six blocks too (26.4).
+// residual 33 us (0.97), 8192 x 2560 fp16 27.2 (0.71), without a residual 24.4 (0.53);
+// backward 8192 x 2560 fp16 18.0 us (0.71), with the bias gradient 21.6 (0.59: the second
+// kernel and the first one's end), 2048 x 10240 from 32 bits with it 24.7 (0.78); 128 x 128
+// 2.5 us, a launch's time.  Two rows in flight a thread at four blocks an SM: with four
+// rows the backward spills more (22.7 us), with six blocks too (26.4); as it is, the form
+// from 32 bits with the bias gradient spills 16 bytes.
 //
 // Included by libgptlayer.cu after gptlayer.cu, in the same translation unit.
 #pragma once

@@ -10,22 +10,28 @@
 // The forward reads the logits once: each thread keeps a running maximum and
 // rescales its Z and S when it grows, once for 64 bytes at most.  x - m is formed
 // before it is scaled, so that neither a mask of the type's lowest value nor
-// large logits lose the difference.  Sums are fp32, of vocab / 256 terms before they
-// are joined in a tree (a batch's own sums first, for longer rows: 2 % slower at
-// 8192 x 50257 and 5 % at the clocks of a long run).
+// large logits lose the difference.  Sums are fp32, in pairs, before they are joined
+// in a tree: chains of vocab / 256 terms in a block of 128 threads, half of that in one
+// of 256, of a block's part in a cluster, and of vocab / 64 (256 at most) where a warp
+// takes the row.  (A batch's own sums first, for longer rows: 2 % slower at 8192 x 50257
+// and 5 % at the clocks of a long run.)
 //
-// Bound by HBM (2 or 4 bytes an element forward, twice that backward), with
-// one exponential an element close behind (16 a clock and SM: 0.72 of the unit's
-// rate at 16-bit logits) and about 8 instructions.  A block takes a row, or a warp
+// Bytes: 2 or 4 an element forward, twice that backward; one exponential (16 a clock
+// and SM) and about 8 instructions.  32-bit logits and the gradient wait for HBM; the
+// forward of 16-bit logits waits for issue slots and the exponential unit (0.72 of
+// its rate) before it waits for memory, so that it follows the SM's clock.  A block takes a row, or a warp
 // where rows are short; with few rows a cluster of up to 8 blocks shares one and joins
 // its parts through distributed shared memory, in one launch without scratch.  In the
 // gradient a warp takes a part of a row.
 //
 // B200, GPU time (share of the bytes at 6535 GB/s): forward with entropy 8192 x 50257
-// bf16 136 us (0.93), 1000 x 32000 fp32 25.1 (0.78), with 5 alternatives 30 (0.65),
-// 2048 x 50257 bf16 43 (0.73), with 20 alternatives 65 (0.48), 8192 x 1000 7.7 (0.33),
-// 5 x 50257 4.4 us, with 20 alternatives 8.8; gradient 4096 x 50257 bf16 138 us (0.91),
-// 2048 x 50304 fp32 132 (0.96), 8192 x 1000 bf16 8.9 (0.57).
+// bf16 136 us in short runs (0.93) and 164 (0.77) in a loop that lasts, where the card
+// reaches its power cap and lowers its clock; 1000 x 32000 fp32 24.2 (0.81), with 5
+// alternatives 30 (0.65), 2048 x 50257 bf16 40 (0.79), with 20 alternatives 61 (0.51),
+// 8192 x 1000 7.7 (0.33: a warp's row is four vectors a lane, and its loads, its join and
+// its results follow one another), 8192 x 4000 18.7 (0.54), 5 x 50257 4.3 us, with 20
+// alternatives 9.2; gradient 4096 x 50257 bf16 138 us (0.91), in a loop 143, 2048 x 50304
+// fp32 132 (0.96), 8192 x 1000 bf16 8.7 (0.58).
 //
 // Top alternatives: a thread remembers in which vector it saw its maximum.  The
 // k-th largest of 64 groups' maxima (as 64-bit keys: value, then lowest index)

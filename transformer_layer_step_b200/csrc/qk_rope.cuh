@@ -19,13 +19,20 @@
 // these are worked on.
 //
 // B200, GPU time (share of the bytes at 6535 GB/s): forward 8192 tokens x 4 groups x
-// (4 + 4 + 4) heads of 64 fp16 21.0 us (0.73), 2048 x 4 x (20 + 20) of 128 bf16 32.0
-// (0.80); backward with gains 2048 x 4 x (20 + 20) of 128 48.8 (0.79), 5003 x (32 + 8 +
-// 8) of 80 32.6 (0.51; five lanes a head), of 64 21.9 (0.54); 16 tokens x (32 + 8) of 128
-// 3.4 us, a launch's time.  The backward with gains is bound by latency: 128 registers
-// allow 16 warps an SM, and issue is half used.  Tried and slower there: rings of
-// asynchronous copies (58 us at 10240), bulk copies of tiles into shared memory (63),
-// three blocks an SM (92, spills), forming dn x twice to save registers (51).
+// (4 + 4 + 4) heads of 64 fp16 21.2 us (0.73; in place 17.1), 2048 x 4 x (20 + 20) of 128
+// bf16 32.0 (0.80); backward with gains 2048 x 4 x (20 + 20) of 128 49.3 (0.78), 5003 x
+// (32 + 8 + 8) of 80 33.0 (0.50), of 64 21.9 (0.54); 16 tokens x (32 + 8) of 128 3.5 us, a
+// launch's time.  Rotation alone: the same forwards 19.9 (0.77; in place 15.3) and 31.5
+// (0.82), backward 31.7 (0.81) and 5003 tokens of 80 19.3 (0.61).
+// What bounds it is latency.  The next slot is fetched ahead only within a token: a
+// token's first loads, its positions and its angles follow one another, every 20 slots
+// at (20 + 20) heads of 128, but every 2 at 8192 x 4 x 4 and every 6 (queries) and 2 (keys)
+// at 32 + 8 of 80, where the eight key heads also fill only 8 of 12 places.  The
+// backward with gains has 128 registers, which allow 16 warps an SM to hide that; issue
+// is half used.  Tried and slower there: rings of asynchronous copies (58 us at
+// 10240), bulk copies of tiles into shared memory (63), three blocks an SM (92, spills),
+// forming dn x twice to save registers (51).  What is kept spills little: 4 to 8 bytes
+// with gains at 5, 6, 9 and 10 lanes backward, 4 bytes forward at a power of two.
 //
 // Included by libgptlayer.cu after gptlayer.cu, in the same translation unit.
 #pragma once
@@ -39,7 +46,7 @@ namespace gptl {
 constexpr int kQkWarps = 8;             // warps of a block
 constexpr int kQkMaxBlocks = 592;       // partial rows of the gains' gradients
 // Blocks resident on an SM, by registers: the forward takes 64, the backward 80, or
-// 128 with the gains' gradients (at 80 that one spills: 49 -> 92 us).
+// 128 with the gains' gradients (at 80 that one spills far more: 49 -> 92 us).
 constexpr int qk_blocks(bool bwd, bool norm) { return !bwd ? 4 : norm ? 2 : 3; }
 constexpr double kQkAngles = 1.0;       // cost of a token's angles, in slots
 
@@ -91,8 +98,10 @@ __device__ __forceinline__ void qk_load_turns(const QkParams &p, QkTurns &t) {
 // Sines and cosines of one token's pairs, by the whole warp.  Lane c of a head
 // holds pairs 8c .. 8c + 7; cs[i * lanes + c] = cosines of its pairs 2i and 2i + 1,
 // then their sines, so that the lanes of a head read 16 neighbouring bytes each.
-// sin.approx and cos.approx are good to 2^-20 in [-pi, pi], a hundredth of a
-// rounding step of the outputs and less.
+// The fast sine and cosine are documented as good to 2^-21.41 and 2^-21.19 absolute
+// in [-pi, pi], and phi's three fp32 roundings are up to 2^-20.8: together a pair turns
+// to within 2^-19 of its larger element, 2^-8 of a half step of fp16 and 2^-11 of bf16.
+// (Of the pair: where a cos - b sin cancels, the result's own step may be smaller.)
 __device__ __forceinline__ void qk_angles(const QkParams &p, const QkTurns &t, int token, float4 *cs,
                                           int lane) {
   __syncwarp();
