@@ -317,8 +317,9 @@ size_t gptl_dropout_scratch_bytes(int rows, int h);
 /* dx (cdt) = dy where kept, times the forward's factor, else 0; dbias (fp32
  * [h], may be NULL, else scratch is needed) = the column sums of that product
  * before it is rounded to dx, in a fixed order; calls that share scratch (those of
- * two captured graphs among them) must be ordered on the device.  dy is fp32 when dy_f32, else
- * cdt; dx may be dy itself where the types agree.  The gradient of resid is dy.
+ * two captured graphs among them) must be ordered on the device.  dy is fp32 when
+ * dy_f32, else cdt; dx may be dy itself where the types agree.  The gradient of
+ * resid is dy.
  * Other arguments and errors as the forward's. */
 int gptl_dropout_add_bwd(int rows, int h, gptl_dtype dtype, const void *dy, int dy_f32, float p,
                          const gptl_rng_state *rng, unsigned site, void *dx, float *dbias,

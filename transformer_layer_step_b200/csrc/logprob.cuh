@@ -381,8 +381,9 @@ __global__ void __launch_bounds__(256, WARP ? 5 : 4) logprob_fwd_kernel(const Lp
     if (tid % width == 0) S.group[tid / width] = g;
     if (tid == 0) S.found = S.hits = 0;
     if (tid < 32) S.best[tid] = 0;
-    // A NaN or +inf in the block's part (their sum is NaN) leaves the row no
-    // alternatives, and an order of keys with NaN among them no k-th: no search.
+    // A NaN or +inf in the block's part makes its sum NaN and leaves the row no
+    // alternatives; the search would not end well, as a NaN may raise a bound that no
+    // number reaches.
     const bool bad_part = __syncthreads_or(!(a.z < INFINITY));
     if (!bad_part) {
       // (empty groups are all 0: the first of equals takes the place)
